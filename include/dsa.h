@@ -534,6 +534,85 @@ DSA_API dsa_status_t dsa_indexer_kl_backward(const void* q_I, const void* k_I, c
                                      size_t workspace_bytes, int32_t* err, dsa_stream_t stream);
 
 /*
+ * Rotary positions.  The queries and keys of the attention, and those of the
+ * indexer, carry their token's position as rotations of pairs of a head's
+ * elements (Su et al., RoFormer, arXiv 2104.09864).  With pair i < rot / 2 of
+ * the rotated part [offset, offset + rot) of a head being its elements (i,
+ * i + rot/2) (interleaved = 0) or (2 i, 2 i + 1) (interleaved = 1), and th =
+ * positions[t] * w_i:
+ *     y_a = rot_scale (x_a cos th - x_b sin th)
+ *     y_b = rot_scale (x_b cos th + x_a sin th)
+ * the other elements pass through, and everything is multiplied by out_scale.
+ * fp32 throughout, one rounding at the end; the angle is reduced exactly at
+ * every 64-bit position.
+ *
+ * Element types of the calls below.
+ */
+#define DSA_TYPE_BF16 0
+#define DSA_TYPE_F32 1
+#define DSA_TYPE_E4M3 2          /* saturating; an infinity becomes NaN */
+
+/* Frequencies for contexts beyond the trained one. */
+#define DSA_ROPE_NONE 0          /* w_i = base^(-2 i / rot) */
+#define DSA_ROPE_LINEAR 1        /* w_i / factor */
+#define DSA_ROPE_NTK 2           /* base * factor^(rot / (rot - 2)) as the base */
+#define DSA_ROPE_YARN 3          /* Peng et al., arXiv 2309.00071: w_i / factor where a pair turns
+                                    fewer than beta_slow times over orig_len positions, w_i where
+                                    more than beta_fast times, linear in between; rot_scale =
+                                    0.1 ln(factor) + 1 */
+
+/*
+ * dsa_rope_freqs - the frequency table of the rotary calls (host function, no
+ * device work): freqs[i] = w_i / (2 pi) turns per position in units of 2^-64,
+ * i < rot / 2, to be copied to the device by the caller; *rot_scale, the
+ * factor on the rotated part, is 1 but for DSA_ROPE_YARN.  factor >= 1 is read
+ * unless scaling is NONE; orig_len, beta_fast and beta_slow only for YARN.
+ * A caller with frequencies of its own fills the same table.
+ */
+DSA_API dsa_status_t dsa_rope_freqs(int rot, double base, int scaling, double factor,
+                                    double orig_len, double beta_fast, double beta_slow,
+                                    uint64_t* freqs, float* rot_scale);
+
+/*
+ * dsa_rope - rotates the heads of one or two arrays that share positions (the
+ * queries and the keys of a layer, or of the indexer).
+ *
+ *   q  [L][Hq][d], k [L][Hk][d]   in_type (BF16 or F32); token t starts at
+ *                                 element t * q_stride (t * k_stride), so the
+ *                                 arrays may be parts of one projection's
+ *                                 output; Hk = 0 (k ignored) for q alone
+ *   positions [L]    int64   device, 8-byte aligned; any values
+ *   freqs [rot / 2]  uint64  device, from dsa_rope_freqs
+ *   q_out, k_out             out_type (BF16, F32 or E4M3), strides as above;
+ *                            may be q and k themselves (same type and
+ *                            stride), and must not overlap them otherwise
+ * d, offset, rot even, offset + rot <= d <= 1024, Hq + Hk <= 1024.  Pointers
+ * aligned to their elements suffice; 16-byte alignment of pointers and
+ * strides, offset and rot multiples of 16 and d of 8 run fastest.  L = 0 does
+ * nothing.
+ */
+DSA_API dsa_status_t dsa_rope(const void* q, const void* k, const int64_t* positions,
+                              const uint64_t* freqs, int64_t L, int Hq, int Hk, int d,
+                              int offset, int rot, int interleaved, float rot_scale,
+                              float out_scale, int in_type, int out_type, int64_t q_stride,
+                              int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                              void* q_out, void* k_out, int32_t* err, dsa_stream_t stream);
+
+/*
+ * dsa_rope_backward - gradients of a loss with respect to dsa_rope's q and k
+ * (out_scale 1) from those with respect to its outputs (such as dQ and dK of
+ * dsa_sparse_attn_backward): the same map with the angles negated.  Arguments
+ * as dsa_rope; out_type BF16 or F32.
+ */
+DSA_API dsa_status_t dsa_rope_backward(const void* dq, const void* dk, const int64_t* positions,
+                                       const uint64_t* freqs, int64_t L, int Hq, int Hk, int d,
+                                       int offset, int rot, int interleaved, float rot_scale,
+                                       int in_type, int out_type, int64_t dq_stride,
+                                       int64_t dk_stride, int64_t dq_out_stride,
+                                       int64_t dk_out_stride, void* dq_out, void* dk_out,
+                                       int32_t* err, dsa_stream_t stream);
+
+/*
  * dsa_check_device_error - synchronizes `stream`, then reads the device
  * error word `err` (a caller's word as passed to the launching calls, or
  * NULL for the current device's library word) into *code (DSA_DEVERR_*) and

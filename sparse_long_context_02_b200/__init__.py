@@ -40,6 +40,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i64, i32, f32, sz = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float,
                                  ctypes.c_size_t)
+        f64 = ctypes.c_double
         L.dsa_version.restype = i32
         L.dsa_version.argtypes = []
         L.dsa_status_string.restype = ctypes.c_char_p
@@ -105,6 +106,15 @@ def lib() -> ctypes.CDLL:
                                             f32, vp, vp, vp, sz, vp, vp]
         L.dsa_decode_combine_shards.restype = i32
         L.dsa_decode_combine_shards.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.dsa_rope_freqs.restype = i32
+        L.dsa_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp,
+                                     ctypes.POINTER(f32)]
+        L.dsa_rope.restype = i32
+        L.dsa_rope.argtypes = [vp] * 4 + [i64] + [i32] * 6 + [f32, f32, i32, i32] + [i64] * 4 + [
+            vp] * 4
+        L.dsa_rope_backward.restype = i32
+        L.dsa_rope_backward.argtypes = [vp] * 4 + [i64] + [i32] * 6 + [f32, i32, i32] + [
+            i64] * 4 + [vp] * 4
         L.dsa_check_device_error.restype = i32
         L.dsa_check_device_error.argtypes = [vp, ctypes.POINTER(i32), vp]
         _lib = L
@@ -541,3 +551,120 @@ def decode_combine_shards(part_o, part_ml, O=None, stream=None, err=None):
                                            P, B, Hq, d, _dev(O, "O", 2), _err(err),
                                            _stream(stream)), "dsa_decode_combine_shards")
     return O
+
+
+# ------------------------------------------------------------------ rotary positions
+
+TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float8_e4m3fn: 2}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _alloc(shape, dtype, device, stream) -> torch.Tensor:
+    """A device tensor that belongs to the launch stream, so that its memory
+    is not handed out again before the stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
+                  else torch.cuda.default_stream())
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _heads(t: torch.Tensor, name: str, L: int, d: int, dtype: torch.dtype):
+    """Pointer and token stride of an array [L][heads][d] whose heads are
+    dense (a part of a wider row is fine)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the library launches on the current "
+                         f"device cuda:{torch.cuda.current_device()}")
+    if t.dim() != 3 or t.shape[0] != L or t.shape[2] != d:
+        raise ValueError(f"{name} must be [{L}][heads][{d}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    H = t.shape[1]
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and H > 1):
+        raise ValueError(f"{name}: each token's heads must be dense, got strides {st}")
+    return t.data_ptr(), (st[0] if L > 1 else H * d), H
+
+
+def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               device=None):
+    """The frequency table of the rotary calls (rot / 2 int64 on the device:
+    turns per position in units of 2^-64) and the factor on the rotated part
+    (`rot_scale`).  scaling: "none", "linear", "ntk" or "yarn"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"rope_freqs: scaling must be one of {sorted(ROPE_SCALINGS)}")
+    freqs = torch.empty(max(0, int(rot)) // 2, dtype=torch.int64)
+    m = ctypes.c_float(1.0)
+    _check(lib().dsa_rope_freqs(int(rot), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                float(orig_len), float(beta_fast), float(beta_slow),
+                                freqs.data_ptr() or None, ctypes.byref(m)), "dsa_rope_freqs")
+    return freqs.to(device if device is not None else "cuda"), m.value
+
+
+def _rope(name, q, k, positions, freqs, rot_scale, out_scale, offset, interleaved, out_dtype,
+          q_out, k_out, stream, err):
+    L, Hq, d = q.shape
+    if q.dtype not in TYPE_CODES:
+        raise ValueError(f"{name}: unsupported dtype {q.dtype}")
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else q.dtype
+    if out_dtype not in TYPE_CODES:
+        raise ValueError(f"{name}: unsupported out_dtype {out_dtype}")
+    if positions.dtype != torch.int64 or positions.numel() != L:
+        raise ValueError(f"{name}: positions must be {L} int64")
+    if freqs.dtype != torch.int64:
+        raise ValueError(f"{name}: freqs must be int64 (rope_freqs)")
+    qp, qs, _ = _heads(q, "q", L, d, q.dtype)
+    if q_out is None:
+        q_out = _alloc((L, Hq, d), out_dtype, q.device, stream)
+    qop, qos, Hqo = _heads(q_out, "q_out", L, d, out_dtype)
+    kp = kop = None
+    ks = kos = Hk = 0
+    if k is not None:
+        kp, ks, Hk = _heads(k, "k", L, d, q.dtype)
+        if k_out is None:
+            k_out = _alloc((L, Hk, d), out_dtype, q.device, stream)
+        kop, kos, Hko = _heads(k_out, "k_out", L, d, out_dtype)
+        if Hko != Hk:
+            raise ValueError(f"{name}: k_out has {Hko} heads, k {Hk}")
+    elif k_out is not None:
+        raise ValueError(f"{name}: k_out without k")
+    if Hqo != Hq:
+        raise ValueError(f"{name}: q_out has {Hqo} heads, q {Hq}")
+    scales = (rot_scale, out_scale) if out_scale is not None else (rot_scale,)
+    _check(getattr(lib(), name)(
+        qp, kp, _dev(positions, "positions", 8), _dev(freqs, "freqs", 8), L, Hq, Hk, d, offset,
+        2 * freqs.numel(), 1 if interleaved else 0, *scales, TYPE_CODES[q.dtype],
+        TYPE_CODES[out_dtype], qs, ks, qos, kos, qop, kop, _err(err), _stream(stream)), name)
+    return q_out, k_out
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+         freqs: torch.Tensor, rot_scale: float = 1.0, out_scale: float = 1.0, offset: int = 0,
+         interleaved: bool = False, out_dtype: Optional[torch.dtype] = None,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None,
+         err=None):
+    """Rotary positions of q [L][Hq][d] and k [L][Hk][d] (or None), bf16 or
+    float32, whose tokens may lie apart (parts of one projection's output).
+    positions [L] int64; freqs and rot_scale from rope_freqs; the rotated part
+    is [offset, offset + 2 len(freqs)) of each head.  out_dtype bfloat16,
+    float32 or float8_e4m3fn (the indexer's q_I and k_I, times out_scale).
+    q_out / k_out may be q and k themselves.  Returns (q_out, k_out)."""
+    return _rope("dsa_rope", q, k, positions, freqs, rot_scale, out_scale, offset, interleaved,
+                 out_dtype, q_out, k_out, stream, err)
+
+
+def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
+                  freqs: torch.Tensor, rot_scale: float = 1.0, offset: int = 0,
+                  interleaved: bool = False, out_dtype: Optional[torch.dtype] = None,
+                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                  stream=None, err=None):
+    """Gradients with respect to rope's q and k (out_scale 1) from those with
+    respect to its outputs (such as sparse_attn_backward's dQ and dK)."""
+    return _rope("dsa_rope_backward", dq, dk, positions, freqs, rot_scale, None, offset,
+                 interleaved, out_dtype, q_out, k_out, stream, err)

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -20,6 +21,7 @@
 #include "sparse_attn_bwd.cuh"
 #include "indexer_kl.cuh"
 #include "indexer_kl_tc.cuh"
+#include "rope.cuh"
 
 namespace {
 
@@ -1362,6 +1364,163 @@ dsa_status_t dsa_indexer_kl_backward(const void* q_I, const void* k_I, const flo
     const dsa_status_t r =
         d_I == 128 ? launch_kl_backward<128>(fn, p, st) : launch_kl_backward<64>(fn, p, st);
     return r == DSA_OK ? ok() : r;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ rotary positions
+
+namespace {
+
+#define CHECK_PTR4(p)                                                                 \
+    do {                                                                              \
+        if ((p) == nullptr) return fail(DSA_ERR_INVALID_ARG, "%s: " #p " is NULL", fn); \
+        if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)                                \
+            return fail(DSA_ERR_INVALID_ARG, "%s: " #p " is not 4-byte aligned", fn);   \
+    } while (0)
+
+int type_bytes(int type) {
+    return type == DSA_TYPE_BF16 ? 2 : type == DSA_TYPE_F32 ? 4 : type == DSA_TYPE_E4M3 ? 1 : 0;
+}
+
+template <typename TI, typename TO>
+dsa_status_t launch_rope(const char* fn, dsa::rope::Params p, cudaStream_t st) {
+    // tokens per CTA: 2 while that leaves a CTA for every SM
+    p.tokens = p.L >= 2 * num_sms() ? 2 : 1;
+    const int64_t grid = (p.L + p.tokens - 1) / p.tokens;
+    const size_t smem = (size_t)p.tokens * (p.rot / 2) * sizeof(float2);
+    dsa::rope::rope_kernel<TI, TO><<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
+    CUDA_TRY(cudaGetLastError());
+    return ok();
+}
+
+dsa_status_t run_rope(const char* fn, const void* q, const void* k, const int64_t* positions,
+                      const uint64_t* freqs, int64_t L, int Hq, int Hk, int d, int offset,
+                      int rot, int interleaved, int inverse, float rot_scale, float out_scale,
+                      int in_type, int out_type, int64_t q_stride, int64_t k_stride,
+                      int64_t q_out_stride, int64_t k_out_stride, void* q_out, void* k_out,
+                      int32_t* err, dsa_stream_t stream) {
+    CHECK_ERR_WORD(err);
+    if (L < 0 || L > (int64_t(1) << 30)) return fail(DSA_ERR_INVALID_ARG, "%s: L = %lld", fn, (long long)L);
+    if (Hq < 1 || Hk < 0 || Hq + Hk > 1024)
+        return fail(DSA_ERR_INVALID_ARG, "%s: Hq = %d, Hk = %d", fn, Hq, Hk);
+    if (d < 2 || d > 1024 || d % 2) return fail(DSA_ERR_INVALID_ARG, "%s: d = %d", fn, d);
+    if (offset < 0 || offset % 2 || rot < 2 || rot % 2 || offset + rot > d)
+        return fail(DSA_ERR_INVALID_ARG, "%s: rotated part [%d, %d + %d) of %d", fn, offset, offset,
+                    rot, d);
+    if (!std::isfinite(rot_scale) || !std::isfinite(out_scale))
+        return fail(DSA_ERR_INVALID_ARG, "%s: rot_scale, out_scale", fn);
+    if (in_type != DSA_TYPE_BF16 && in_type != DSA_TYPE_F32)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: in_type = %d", fn, in_type);
+    if (type_bytes(out_type) == 0 || (inverse && out_type == DSA_TYPE_E4M3))
+        return fail(DSA_ERR_UNSUPPORTED, "%s: out_type = %d", fn, out_type);
+    if (L == 0) return ok();
+    const int ib = type_bytes(in_type), ob = type_bytes(out_type);
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
+    const int H[2] = {Hq, Hk};
+    dsa::rope::Params p{};
+    for (int w = 0; w < 2 && H[w] > 0; ++w) {
+        if (in[w] == nullptr || out[w] == nullptr)
+            return fail(DSA_ERR_INVALID_ARG, "%s: %s is NULL", fn,
+                        w ? (in[w] ? "k_out" : "k") : (in[w] ? "q_out" : "q"));
+        if (reinterpret_cast<uintptr_t>(in[w]) % ib || reinterpret_cast<uintptr_t>(out[w]) % ob)
+            return fail(DSA_ERR_INVALID_ARG, "%s: %s is not aligned to its elements", fn,
+                        w ? "k or k_out" : "q or q_out");
+        if (is[w] < (int64_t)H[w] * d || os[w] < (int64_t)H[w] * d)
+            return fail(DSA_ERR_INVALID_ARG, "%s: a token stride below heads x d", fn);
+        p.x[w] = in[w];
+        p.y[w] = out[w];
+        p.xs[w] = is[w];
+        p.ys[w] = os[w];
+        p.H[w] = H[w];
+    }
+    if (positions == nullptr || freqs == nullptr || (reinterpret_cast<uintptr_t>(positions) & 7u) ||
+        (reinterpret_cast<uintptr_t>(freqs) & 7u))
+        return fail(DSA_ERR_INVALID_ARG, "%s: positions or freqs is NULL or not 8-byte aligned", fn);
+    p.pos = positions;
+    p.freqs = freqs;
+    p.L = L;
+    p.d = d;
+    p.off = offset;
+    p.rot = rot;
+    p.interleaved = interleaved != 0;
+    p.inverse = inverse;
+    p.rot_scale = rot_scale;
+    p.out_scale = out_scale;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    using bf = __nv_bfloat16;
+    if (in_type == DSA_TYPE_BF16) {
+        if (out_type == DSA_TYPE_BF16) return launch_rope<bf, bf>(fn, p, st);
+        if (out_type == DSA_TYPE_F32) return launch_rope<bf, float>(fn, p, st);
+        return launch_rope<bf, __nv_fp8_e4m3>(fn, p, st);
+    }
+    if (out_type == DSA_TYPE_BF16) return launch_rope<float, bf>(fn, p, st);
+    if (out_type == DSA_TYPE_F32) return launch_rope<float, float>(fn, p, st);
+    return launch_rope<float, __nv_fp8_e4m3>(fn, p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status_t dsa_rope_freqs(int rot, double base, int scaling, double factor, double orig_len,
+                            double beta_fast, double beta_slow, uint64_t* freqs,
+                            float* rot_scale) {
+    static const char fn[] = "dsa_rope_freqs";
+    const double two_pi = 6.283185307179586476925286766559;
+    if (freqs == nullptr || rot_scale == nullptr)
+        return fail(DSA_ERR_INVALID_ARG, "%s: freqs or rot_scale is NULL", fn);
+    if (rot < 2 || rot % 2 || rot > 1024) return fail(DSA_ERR_INVALID_ARG, "%s: rot = %d", fn, rot);
+    if (!(base > 1.0) || !(base < 1e30)) return fail(DSA_ERR_INVALID_ARG, "%s: base", fn);
+    if (scaling < DSA_ROPE_NONE || scaling > DSA_ROPE_YARN)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: scaling = %d", fn, scaling);
+    if (scaling != DSA_ROPE_NONE && (!(factor >= 1.0) || !(factor < 1e9)))
+        return fail(DSA_ERR_INVALID_ARG, "%s: factor", fn);
+    if (scaling == DSA_ROPE_NTK && rot < 4)
+        return fail(DSA_ERR_INVALID_ARG, "%s: rot = %d with a scaled base", fn, rot);
+    if (scaling == DSA_ROPE_YARN &&
+        (!(orig_len >= 1.0) || !(orig_len < 1e15) || !(beta_slow >= 0.0) ||
+         !(beta_fast > beta_slow) || !(beta_fast < 1e15)))
+        return fail(DSA_ERR_INVALID_ARG, "%s: orig_len, beta_fast or beta_slow", fn);
+    if (scaling == DSA_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double w = std::pow(base, -2.0 * i / rot);
+        if (scaling == DSA_ROPE_LINEAR) w /= factor;
+        if (scaling == DSA_ROPE_YARN) {
+            const double turns = orig_len * w / two_pi;
+            double g = (turns - beta_slow) / (beta_fast - beta_slow);
+            g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+            w = (1.0 - g) * w / factor + g * w;
+        }
+        // w <= 1 rad, so the fraction is below 0.16 turns and fits
+        freqs[i] = (uint64_t)std::llrint(w / two_pi * 18446744073709551616.0);
+    }
+    *rot_scale = scaling == DSA_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return ok();
+}
+
+dsa_status_t dsa_rope(const void* q, const void* k, const int64_t* positions,
+                      const uint64_t* freqs, int64_t L, int Hq, int Hk, int d, int offset,
+                      int rot, int interleaved, float rot_scale, float out_scale, int in_type,
+                      int out_type, int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                      int64_t k_out_stride, void* q_out, void* k_out, int32_t* err,
+                      dsa_stream_t stream) {
+    return run_rope("dsa_rope", q, k, positions, freqs, L, Hq, Hk, d, offset, rot, interleaved, 0,
+                    rot_scale, out_scale, in_type, out_type, q_stride, k_stride, q_out_stride,
+                    k_out_stride, q_out, k_out, err, stream);
+}
+
+dsa_status_t dsa_rope_backward(const void* dq, const void* dk, const int64_t* positions,
+                               const uint64_t* freqs, int64_t L, int Hq, int Hk, int d,
+                               int offset, int rot, int interleaved, float rot_scale,
+                               int in_type, int out_type, int64_t dq_stride, int64_t dk_stride,
+                               int64_t dq_out_stride, int64_t dk_out_stride, void* dq_out,
+                               void* dk_out, int32_t* err, dsa_stream_t stream) {
+    return run_rope("dsa_rope_backward", dq, dk, positions, freqs, L, Hq, Hk, d, offset, rot,
+                    interleaved, 1, rot_scale, 1.f, in_type, out_type, dq_stride, dk_stride,
+                    dq_out_stride, dk_out_stride, dq_out, dk_out, err, stream);
 }
 
 }  // extern "C"
