@@ -613,6 +613,49 @@ DSA_API dsa_status_t dsa_rope_backward(const void* dq, const void* dk, const int
                                        int32_t* err, dsa_stream_t stream);
 
 /*
+ * A paged K/V cache in 8 bits.  The caller owns two pools of pages and hands
+ * them to sequences through a block table:
+ *
+ *   K8, V8       [num_pages][page][Hkv][d]  e4m3 codes
+ *   k_scale, v_scale [num_pages][Hkv]       fp32, positive: a stored element
+ *                                           is code * scale of its page and head
+ *   block_table  [B][max_pages]  int32  device: page of positions
+ *                                [c page, (c + 1) page) of sequence b at [b][c];
+ *                                entries past a sequence's length are not read
+ *   seq_lens     [B]             int32  device
+ * page in {16, 32, 64, 128}, d in {64, 128}, Hkv <= 64, num_pages * page <
+ * 2^31.  Pools and rows are 16-byte, the int32 and fp32 arrays 4-byte aligned.
+ * A page that a position needs but whose table entry is outside [0,
+ * num_pages), or that lies past max_pages, is left out and recorded as
+ * DSA_DEVERR_INDEX.
+ *
+ * dsa_kv8_append - quantises new K and V rows and stores them behind each
+ * sequence's seq_lens[b] tokens (the lengths before the call; the caller adds
+ * the new tokens afterwards).
+ *
+ *   K, V  [T][Hkv][d] bf16; row r starts at element r * k_stride (r * v_stride),
+ *         strides multiples of 8
+ *   new_off [B + 1] int32 device: rows [new_off[b], new_off[b + 1]) are
+ *         sequence b's, ascending from 0 to at most T; or NULL: T = B, one
+ *         row for each sequence.  Rows past new_off[B] are ignored.
+ *   seq_lens[b] < 0: an idle place of the batch, skipped with its rows.
+ * Per page, head and tensor: need = the smallest power of two (2^-120 at
+ * least) with max |new finite elements on the page| <= 448 need; the scale
+ * becomes need on a page that held no token, else max(scale, need), and where
+ * that is larger than before the older tokens' codes are rounded again under
+ * it.  New codes are x / scale (in fp32) rounded to nearest even; a NaN or an
+ * infinity is stored as NaN.  Slots without a token are left as they are.
+ * A page may be shared by several sequences' tables only where none of them
+ * appends to it.  T = 0 does nothing.
+ */
+DSA_API dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int64_t k_stride,
+                                    int64_t v_stride, void* K8, void* V8, float* k_scale,
+                                    float* v_scale, int64_t num_pages, int page,
+                                    const int32_t* block_table, int max_pages,
+                                    const int32_t* seq_lens, const int32_t* new_off, int B,
+                                    int Hkv, int d, int32_t* err, dsa_stream_t stream);
+
+/*
  * dsa_check_device_error - synchronizes `stream`, then reads the device
  * error word `err` (a caller's word as passed to the launching calls, or
  * NULL for the current device's library word) into *code (DSA_DEVERR_*) and

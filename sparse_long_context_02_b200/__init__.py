@@ -115,6 +115,9 @@ def lib() -> ctypes.CDLL:
         L.dsa_rope_backward.restype = i32
         L.dsa_rope_backward.argtypes = [vp] * 4 + [i64] + [i32] * 6 + [f32, i32, i32] + [
             i64] * 4 + [vp] * 4
+        L.dsa_kv8_append.restype = i32
+        L.dsa_kv8_append.argtypes = [vp, vp] + [i64] * 3 + [vp] * 4 + [i64, i32, vp, i32, vp, vp,
+                                                                     i32, i32, i32, vp, vp]
         L.dsa_check_device_error.restype = i32
         L.dsa_check_device_error.argtypes = [vp, ctypes.POINTER(i32), vp]
         _lib = L
@@ -668,3 +671,57 @@ def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch
     respect to its outputs (such as sparse_attn_backward's dQ and dK)."""
     return _rope("dsa_rope_backward", dq, dk, positions, freqs, rot_scale, None, offset,
                  interleaved, out_dtype, q_out, k_out, stream, err)
+
+
+# ------------------------------------------------------------------ 8-bit cache
+
+def _pools(k8, v8, k_scale, v_scale, block_table, seq_lens):
+    """Checks a cache's pools and tables; returns the pointers and sizes."""
+    if k8.dim() != 4 or v8.shape != k8.shape:
+        raise ValueError("k8 and v8 must be [pages][page][Hkv][d] of one shape, got "
+                         f"{tuple(k8.shape)} and {tuple(v8.shape)}")
+    P, page, Hkv, d = k8.shape
+    for t, name in ((k8, "k8"), (v8, "v8")):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype != torch.float32 or t.shape != (P, Hkv):
+            raise ValueError(f"{name} must be [{P}][{Hkv}] float32")
+    for t, name, dims in ((block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
+        if t.dtype != torch.int32 or t.dim() != dims:
+            raise ValueError(f"{name} must be int32 with {dims} dimension(s)")
+    B, M = block_table.shape
+    if seq_lens.shape[0] != B:
+        raise ValueError(f"seq_lens must have {B} entries, one per block_table row")
+    return ((_dev(k8, "k8", 1), _dev(v8, "v8", 1), _dev(k_scale, "k_scale", 4),
+             _dev(v_scale, "v_scale", 4)),
+            (_dev(block_table, "block_table", 4), M, _dev(seq_lens, "seq_lens", 4)),
+            P, page, Hkv, d, B)
+
+
+def _offsets(t: Optional[torch.Tensor], name: str, B: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != B + 1:
+        raise ValueError(f"{name} must be {B + 1} int32")
+    return _dev(t, name, 4)
+
+
+def kv8_append(K: torch.Tensor, V: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor,
+               k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+               seq_lens: torch.Tensor, new_off: Optional[torch.Tensor] = None, stream=None,
+               err=None) -> None:
+    """Quantises new rows K, V [T][Hkv][d] (bf16, tokens may lie apart) and
+    stores them in the paged 8-bit cache behind seq_lens[b] tokens of each
+    sequence: rows [new_off[b], new_off[b + 1]), or row b without new_off.
+    k8, v8 [pages][page][Hkv][d] e4m3 and k_scale, v_scale [pages][Hkv] are
+    updated in place; seq_lens is not (the caller adds the new tokens)."""
+    pools, seqs, P, page, Hkv, d, B = _pools(k8, v8, k_scale, v_scale, block_table, seq_lens)
+    T = K.shape[0]
+    kp, ks, Hk = _heads(K, "K", T, d, torch.bfloat16)
+    vp, vs, Hv = _heads(V, "V", T, d, torch.bfloat16)
+    if Hk != Hkv or Hv != Hkv:
+        raise ValueError(f"K and V must have {Hkv} heads")
+    _check(lib().dsa_kv8_append(kp, vp, T, ks, vs, *pools, P, page, *seqs,
+                                _offsets(new_off, "new_off", B), B, Hkv, d, _err(err),
+                                _stream(stream)), "dsa_kv8_append")

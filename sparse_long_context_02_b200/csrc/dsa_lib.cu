@@ -21,6 +21,7 @@
 #include "sparse_attn_bwd.cuh"
 #include "indexer_kl.cuh"
 #include "indexer_kl_tc.cuh"
+#include "kv8.cuh"
 #include "rope.cuh"
 
 namespace {
@@ -1521,6 +1522,94 @@ dsa_status_t dsa_rope_backward(const void* dq, const void* dk, const int64_t* po
     return run_rope("dsa_rope_backward", dq, dk, positions, freqs, L, Hq, Hk, d, offset, rot,
                     interleaved, 1, rot_scale, 1.f, in_type, out_type, dq_stride, dk_stride,
                     dq_out_stride, dk_out_stride, dq_out, dk_out, err, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ 8-bit cache
+
+namespace {
+
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+
+template <int PAGE, int D>
+dsa_status_t launch_append(const char* fn, const dsa::kv8::AppendParams& p, int64_t units,
+                           cudaStream_t st) {
+    dsa::kv8::append_kernel<PAGE, D>
+        <<<dim3((unsigned)(units * p.Hkv), 2), dsa::kv8::AppendCfg<PAGE, D>::THREADS, 0, st>>>(p);
+    CUDA_TRY(cudaGetLastError());
+    return ok();
+}
+
+template <int D>
+dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendParams& p,
+                             int64_t units, cudaStream_t st) {
+    if (page == 16) return launch_append<16, D>(fn, p, units, st);
+    if (page == 32) return launch_append<32, D>(fn, p, units, st);
+    if (page == 64) return launch_append<64, D>(fn, p, units, st);
+    return launch_append<128, D>(fn, p, units, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int64_t k_stride,
+                            int64_t v_stride, void* K8, void* V8, float* k_scale, float* v_scale,
+                            int64_t num_pages, int page, const int32_t* block_table,
+                            int max_pages, const int32_t* seq_lens, const int32_t* new_off, int B,
+                            int Hkv, int d, int32_t* err, dsa_stream_t stream) {
+    static const char fn[] = "dsa_kv8_append";
+    CHECK_ERR_WORD(err);
+    if (T < 0 || T > (int64_t(1) << 30) || B < 0 || B > (1 << 24))
+        return fail(DSA_ERR_INVALID_ARG, "%s: T = %lld, B = %d", fn, (long long)T, B);
+    if (Hkv < 1) return fail(DSA_ERR_INVALID_ARG, "%s: Hkv = %d", fn, Hkv);
+    if ((d != 64 && d != 128) || Hkv > 64 || !page_ok(page))
+        return fail(DSA_ERR_UNSUPPORTED,
+                    "%s: supported d in {64, 128}, Hkv <= 64, page in {16, 32, 64, 128}; got d = "
+                    "%d, Hkv = %d, page = %d", fn, d, Hkv, page);
+    if (T == 0) return ok();
+    if (num_pages < 1 || num_pages * page >= (int64_t(1) << 31) || max_pages < 1 ||
+        (int64_t)max_pages * page >= (int64_t(1) << 31))
+        return fail(DSA_ERR_INVALID_ARG, "%s: num_pages = %lld, max_pages = %d", fn,
+                    (long long)num_pages, max_pages);
+    if (B < 1 || (new_off == nullptr && T != B))
+        return fail(DSA_ERR_INVALID_ARG, "%s: T = %lld rows for B = %d sequences without new_off", fn,
+                    (long long)T, B);
+    CHECK_PTR(K);
+    CHECK_PTR(V);
+    CHECK_PTR(K8);
+    CHECK_PTR(V8);
+    CHECK_PTR4(k_scale);
+    CHECK_PTR4(v_scale);
+    CHECK_PTR4(block_table);
+    CHECK_PTR4(seq_lens);
+    if (new_off != nullptr) CHECK_PTR4(new_off);
+    if (k_stride < (int64_t)Hkv * d || v_stride < (int64_t)Hkv * d || k_stride % 8 || v_stride % 8)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "%s: k_stride = %lld, v_stride = %lld (multiples of 8, at least Hkv x d)", fn,
+                    (long long)k_stride, (long long)v_stride);
+    const int64_t units = new_off == nullptr ? B : T / page + 2 * (int64_t)B;
+    if (units * Hkv >= (int64_t(1) << 31)) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
+    dsa::kv8::AppendParams p{};
+    p.x[0] = static_cast<const __nv_bfloat16*>(K);
+    p.x[1] = static_cast<const __nv_bfloat16*>(V);
+    p.xs[0] = k_stride;
+    p.xs[1] = v_stride;
+    p.code[0] = static_cast<uint8_t*>(K8);
+    p.code[1] = static_cast<uint8_t*>(V8);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.rows = {new_off, B, T};
+    p.M = max_pages;
+    p.Hkv = Hkv;
+    p.pages = num_pages;
+    p.err = err;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return d == 128 ? dispatch_append<128>(fn, page, p, units, st)
+                    : dispatch_append<64>(fn, page, p, units, st);
 }
 
 }  // extern "C"
