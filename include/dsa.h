@@ -656,6 +656,67 @@ DSA_API dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int
                                     int Hkv, int d, int32_t* err, dsa_stream_t stream);
 
 /*
+ * dsa_attn_kv8_workspace_size - bytes of device workspace (16-byte aligned;
+ * not read before it is written) for T query rows over at most `keys` keys
+ * each: k for dsa_sparse_attn_kv8, max_pages * page for dsa_attn_kv8.  May be
+ * 0 (the workspace may then be NULL).
+ */
+DSA_API size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int Hkv, int d);
+
+/*
+ * dsa_sparse_attn_kv8 - dsa_sparse_attn_prefill / the attention of
+ * dsa_sparse_attn_decode over the 8-bit cache: for query row t of sequence b,
+ * head h and group g = h / (Hq / Hkv),
+ *   O[t,h] = sum_{s in idx[t]} softmax_s(scale * Q[t,h] . K[s,g]) V[s,g]
+ * with the sequence's stored rows K[s], V[s] (an entry that repeats counts
+ * once per entry).
+ *
+ *   Q    [T][Hq][d] bf16
+ *   row_off [B + 1] int32 device: rows [row_off[b], row_off[b + 1]) are
+ *        sequence b's (a chunk of its prompt, or several tokens decoded at
+ *        once), row_off[0] = 0, ascending, at most T; or NULL: T = B, one row
+ *        for each sequence.  O and lse of rows past row_off[B] are not written.
+ *   seq_lens [B]: stored tokens, the rows' own included; <= 0: no keys
+ *   idx  [T][k] int32: positions in the row's sequence (such as
+ *        dsa_decode_select_shard's key_out, or dsa_index_topk's rows);
+ *        entries < 0 are skipped, entries >= seq_lens[b] skipped and recorded
+ *        as DSA_DEVERR_INDEX
+ *   O    [T][Hq][d] bf16 OUT (a row without keys is zeros)
+ *   lse  [T][Hq] fp32 OUT or NULL: natural log of the softmax normaliser,
+ *        -inf for a row without keys
+ *   workspace: dsa_attn_kv8_workspace_size(T, k, Hq, Hkv, d) bytes; calls that
+ *        may overlap on the GPU (two captured graphs included) need one each
+ * Supported: d in {64, 128}, Hq / Hkv <= 8, Hkv <= 64, k <= 65536.  Scores
+ * and softmax statistics are fp32, the softmax weights fp16 for the product
+ * with V's codes.  Deterministic.  T = 0 does nothing.
+ */
+DSA_API dsa_status_t dsa_sparse_attn_kv8(const void* Q, const void* K8, const void* V8,
+                                         const float* k_scale, const float* v_scale,
+                                         int64_t num_pages, int page, const int32_t* block_table,
+                                         int max_pages, const int32_t* seq_lens,
+                                         const int32_t* row_off, int B, int64_t T,
+                                         const int32_t* idx, int k, int Hq, int Hkv, int d,
+                                         float scale, void* O, float* lse, void* workspace,
+                                         size_t workspace_bytes, int32_t* err,
+                                         dsa_stream_t stream);
+
+/*
+ * dsa_attn_kv8 - the same over every key: row t of sequence b attends to the
+ * positions [0, seq_lens[b]), and with row_off, where the rows are the
+ * sequence's last tokens, row j of R to [0, seq_lens[b] - (R - 1 - j))
+ * (causal).  For layers or stages that keep the full attention, and contexts
+ * no longer than the selection.  Arguments and support as
+ * dsa_sparse_attn_kv8, without idx; workspace for max_pages * page keys.
+ */
+DSA_API dsa_status_t dsa_attn_kv8(const void* Q, const void* K8, const void* V8,
+                                  const float* k_scale, const float* v_scale, int64_t num_pages,
+                                  int page, const int32_t* block_table, int max_pages,
+                                  const int32_t* seq_lens, const int32_t* row_off, int B,
+                                  int64_t T, int Hq, int Hkv, int d, float scale, void* O,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  int32_t* err, dsa_stream_t stream);
+
+/*
  * dsa_check_device_error - synchronizes `stream`, then reads the device
  * error word `err` (a caller's word as passed to the launching calls, or
  * NULL for the current device's library word) into *code (DSA_DEVERR_*) and

@@ -80,3 +80,41 @@ def append(x, codes, scales, table, lens, new_off) -> None:
                         codes[p, :first, h] = encode(old / s)
                 codes[p, first:last, h] = encode(part / s)
                 scales[p, h] = s
+
+
+def gather(codes, scales, table, b, keys) -> np.ndarray:
+    """Stored rows [len(keys)][Hkv][d] of sequence b."""
+    page = codes.shape[1]
+    keys = np.asarray(keys, np.int64)
+    p = table[b, keys // page]
+    return decode(codes[p, keys % page]) * np.asarray(scales, np.float64)[p][..., None]
+
+
+def attention(Q, k8, v8, k_scale, v_scale, table, seq, keys, scale):
+    """Rows Q [T][Hq][d] (float64) of sequences seq[t] over their keys[t]
+    (lists of positions).  Returns O, lse and what the error bounds need: per
+    (t, h), the sum of p |v| as an array like O, the largest scale * sum_c
+    |q_c k_c| and the largest weight * v scale."""
+    T, Hq, d = Q.shape
+    Hkv, page = k8.shape[2], k8.shape[1]
+    G = Hq // Hkv
+    O, mag = np.zeros((T, Hq, d)), np.zeros((T, Hq, d))
+    lse = np.full((T, Hq), -np.inf)
+    big, top = np.zeros((T, Hq)), np.zeros((T, Hq))
+    for t in range(T):
+        ks = np.asarray(keys[t], np.int64)
+        if len(ks) == 0:
+            continue
+        K = gather(k8, k_scale, table, seq[t], ks)
+        V = gather(v8, v_scale, table, seq[t], ks)
+        vs = np.asarray(v_scale, np.float64)[table[seq[t], ks // page]]
+        for h in range(Hq):
+            g = h // G
+            x = K[:, g] @ Q[t, h] * scale
+            e = np.exp(x - x.max())
+            p = e / e.sum()
+            O[t, h], mag[t, h] = p @ V[:, g], p @ np.abs(V[:, g])
+            lse[t, h] = x.max() + np.log(e.sum())
+            big[t, h] = (np.abs(K[:, g]) @ np.abs(Q[t, h])).max() * scale
+            top[t, h] = (p * vs[:, g]).max()
+    return O, lse, mag, big, top

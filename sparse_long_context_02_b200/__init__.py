@@ -118,6 +118,14 @@ def lib() -> ctypes.CDLL:
         L.dsa_kv8_append.restype = i32
         L.dsa_kv8_append.argtypes = [vp, vp] + [i64] * 3 + [vp] * 4 + [i64, i32, vp, i32, vp, vp,
                                                                      i32, i32, i32, vp, vp]
+        L.dsa_attn_kv8_workspace_size.restype = sz
+        L.dsa_attn_kv8_workspace_size.argtypes = [i64, i64, i32, i32, i32]
+        kv8 = [vp] * 5 + [i64, i32, vp, i32, vp, vp, i32, i64]
+        L.dsa_sparse_attn_kv8.restype = i32
+        L.dsa_sparse_attn_kv8.argtypes = kv8 + [vp, i32, i32, i32, i32, f32, vp, vp, vp, sz, vp,
+                                                vp]
+        L.dsa_attn_kv8.restype = i32
+        L.dsa_attn_kv8.argtypes = kv8 + [i32, i32, i32, f32, vp, vp, vp, sz, vp, vp]
         L.dsa_check_device_error.restype = i32
         L.dsa_check_device_error.argtypes = [vp, ctypes.POINTER(i32), vp]
         _lib = L
@@ -725,3 +733,66 @@ def kv8_append(K: torch.Tensor, V: torch.Tensor, k8: torch.Tensor, v8: torch.Ten
     _check(lib().dsa_kv8_append(kp, vp, T, ks, vs, *pools, P, page, *seqs,
                                 _offsets(new_off, "new_off", B), B, Hkv, d, _err(err),
                                 _stream(stream)), "dsa_kv8_append")
+
+
+def attn_kv8_workspace_size(T: int, keys: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of workspace for T rows over at most `keys` keys each: k for
+    sparse_attn_kv8, block_table columns x page for attn_kv8."""
+    return lib().dsa_attn_kv8_workspace_size(T, keys, Hq, Hkv, d)
+
+
+def _attn_kv8(name, Q, k8, v8, k_scale, v_scale, block_table, seq_lens, idx, scale, row_off, O,
+              lse, workspace, stream, err):
+    pools, (tp, M, lp), P, page, Hkv, d, B = _pools(k8, v8, k_scale, v_scale, block_table,
+                                                    seq_lens)
+    if Q.dim() != 3 or Q.shape[2] != d or Q.dtype != torch.bfloat16:
+        raise ValueError(f"Q must be [T][Hq][{d}] bfloat16, got {tuple(Q.shape)} {Q.dtype}")
+    T, Hq, _ = Q.shape
+    if O is None:
+        O = _alloc((T, Hq, d), torch.bfloat16, Q.device, stream)
+    elif O.shape != Q.shape or O.dtype != torch.bfloat16:
+        raise ValueError("O must have Q's shape, in bfloat16")
+    if lse is not None and (lse.shape != (T, Hq) or lse.dtype != torch.float32):
+        raise ValueError(f"lse must be [{T}][{Hq}] float32")
+    if idx is not None:
+        if idx.dim() != 2 or idx.shape[0] != T or idx.dtype != torch.int32:
+            raise ValueError(f"idx must be [{T}][k] int32")
+        keys = idx.shape[1]
+        sel = (_dev(idx, "idx", 4), keys)
+    else:
+        keys, sel = M * page, ()
+    need = attn_kv8_workspace_size(T, keys, Hq, Hkv, d)
+    if workspace is None and need:
+        workspace = _alloc(need, torch.uint8, Q.device, stream)
+    ws = (None, 0) if workspace is None else (
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    _check(getattr(lib(), name)(
+        _dev(Q, "Q", 2), *pools, P, page, tp, M, lp, _offsets(row_off, "row_off", B), B, T, *sel,
+        Hq, Hkv, d, float(scale), _dev(O, "O", 2), _dev(lse, "lse", 4) if lse is not None else None,
+        *ws, _err(err), _stream(stream)), name)
+    return O
+
+
+def sparse_attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                    idx: torch.Tensor, scale: float, row_off: Optional[torch.Tensor] = None,
+                    O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    err=None) -> torch.Tensor:
+    """Sparse GQA attention over the paged 8-bit cache: row t of Q [T][Hq][d]
+    attends to positions idx[t] (-1: none) of its sequence, row b of sequence
+    b, or rows [row_off[b], row_off[b + 1]).  Returns O [T][Hq][d]; `lse` as
+    sparse_attn_prefill.  Calls that may overlap need a workspace each."""
+    return _attn_kv8("dsa_sparse_attn_kv8", Q, k8, v8, k_scale, v_scale, block_table, seq_lens,
+                     idx, scale, row_off, O, lse, workspace, stream, err)
+
+
+def attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
+             v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+             scale: float, row_off: Optional[torch.Tensor] = None,
+             O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, stream=None, err=None) -> torch.Tensor:
+    """sparse_attn_kv8 over every key of the sequence; with row_off, where the
+    rows are a sequence's last tokens, causally."""
+    return _attn_kv8("dsa_attn_kv8", Q, k8, v8, k_scale, v_scale, block_table, seq_lens, None,
+                     scale, row_off, O, lse, workspace, stream, err)

@@ -1550,6 +1550,108 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
     return launch_append<128, D>(fn, p, units, st);
 }
 
+// Slices per row: enough CTAs for two per resident slot (four of 128 threads
+// per SM), none shorter than 64 keys.
+int kv8_splits(int64_t T, int64_t cap, int Hkv) {
+    const int64_t want = (int64_t)num_sms() * 8 / (T * Hkv);
+    const int64_t most = (cap + 63) / 64;
+    const int64_t n = want < most ? want : most;
+    return (int)(n < 1 ? 1 : n > 256 ? 256 : n);
+}
+
+size_t kv8_workspace(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
+    const int ns = kv8_splits(T, cap, Hkv);
+    return ns == 1 ? 0 : align256((size_t)T * ns * Hq * d * 4) + align256((size_t)T * ns * Hq * 16);
+}
+
+template <int D>
+dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, cudaStream_t st) {
+    const dim3 grid((unsigned)(p.rows.n * p.Hkv), (unsigned)p.nsplit);
+    if (p.idx != nullptr)
+        dsa::kv8::attn_kernel<D, false><<<grid, dsa::kv8::kWarps * 32, 0, st>>>(p);
+    else
+        dsa::kv8::attn_kernel<D, true><<<grid, dsa::kv8::kWarps * 32, 0, st>>>(p);
+    CUDA_TRY(cudaGetLastError());
+    if (p.nsplit > 1) {
+        CUDA_TRY(launch_chained(dsa::kv8::combine_kernel<D>,
+                                dim3((unsigned)(p.Hkv * p.G), (unsigned)p.rows.n), dim3(D), 0, st,
+                                p));
+        CUDA_TRY(cudaGetLastError());
+    }
+    return ok();
+}
+
+dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const void* V8,
+                          const float* k_scale, const float* v_scale, int64_t num_pages, int page,
+                          const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                          const int32_t* row_off, int B, int64_t T, bool sparse,
+                          const int32_t* idx, int k, int Hq, int Hkv, int d, float scale, void* O,
+                          float* lse, void* workspace, size_t workspace_bytes, int32_t* err,
+                          dsa_stream_t stream) {
+    CHECK_ERR_WORD(err);
+    if (T < 0 || B < 0 || B > (1 << 24)) return fail(DSA_ERR_INVALID_ARG, "%s: T = %lld, B = %d", fn, (long long)T, B);
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv) return fail(DSA_ERR_INVALID_ARG, "%s: Hq = %d, Hkv = %d", fn, Hq, Hkv);
+    if (!(scale > 0.f) || !(scale < 1e30f)) return fail(DSA_ERR_INVALID_ARG, "%s: scale", fn);
+    if (sparse && (k < 1 || k > 65536)) return fail(DSA_ERR_INVALID_ARG, "%s: k = %d", fn, k);
+    if ((d != 64 && d != 128) || Hq / Hkv > 8 || Hkv > 64 || !page_ok(page))
+        return fail(DSA_ERR_UNSUPPORTED,
+                    "%s: supported d in {64, 128}, Hq/Hkv <= 8, Hkv <= 64, page in {16, 32, 64, "
+                    "128}; got d = %d, Hq = %d, Hkv = %d, page = %d", fn, d, Hq, Hkv, page);
+    if (T * Hkv >= (int64_t(1) << 31)) return fail(DSA_ERR_UNSUPPORTED, "%s: T * Hkv too large", fn);
+    if (T == 0) return ok();
+    if (num_pages < 1 || num_pages * page >= (int64_t(1) << 31) || max_pages < 1 ||
+        (int64_t)max_pages * page >= (int64_t(1) << 31))
+        return fail(DSA_ERR_INVALID_ARG, "%s: num_pages = %lld, max_pages = %d", fn,
+                    (long long)num_pages, max_pages);
+    if (B < 1 || (row_off == nullptr && T != B))
+        return fail(DSA_ERR_INVALID_ARG, "%s: T = %lld rows for B = %d sequences without row_off", fn,
+                    (long long)T, B);
+    CHECK_PTR(Q);
+    CHECK_PTR(K8);
+    CHECK_PTR(V8);
+    CHECK_PTR4(k_scale);
+    CHECK_PTR4(v_scale);
+    CHECK_PTR4(block_table);
+    CHECK_PTR4(seq_lens);
+    if (row_off != nullptr) CHECK_PTR4(row_off);
+    if (sparse) CHECK_PTR4(idx);
+    CHECK_PTR(O);
+    if (lse != nullptr) CHECK_PTR4(lse);
+    const int64_t cap = sparse ? k : (int64_t)max_pages * page;
+    const size_t need = kv8_workspace(T, cap, Hq, Hkv, d);
+    if (need > 0) {
+        CHECK_PTR(workspace);
+        if (workspace_bytes < need)
+            return fail(DSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+    }
+    dsa::kv8::AttnParams p{};
+    p.Q = static_cast<const __nv_bfloat16*>(Q);
+    p.code[0] = static_cast<const uint8_t*>(K8);
+    p.code[1] = static_cast<const uint8_t*>(V8);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.idx = sparse ? idx : nullptr;
+    p.rows = {row_off, B, T};
+    p.M = max_pages;
+    p.Hkv = Hkv;
+    p.G = Hq / Hkv;
+    p.k = k;
+    p.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+    p.pages = num_pages;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.nsplit = kv8_splits(T, cap, Hkv);
+    p.O = static_cast<__nv_bfloat16*>(O);
+    p.lse = lse;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_m = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                        align256((size_t)T * p.nsplit * Hq * d * 4));
+    p.err = err;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return d == 128 ? launch_kv8_attn<128>(fn, p, st) : launch_kv8_attn<64>(fn, p, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1610,6 +1712,34 @@ dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int64_t k_s
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return d == 128 ? dispatch_append<128>(fn, page, p, units, st)
                     : dispatch_append<64>(fn, page, p, units, st);
+}
+
+size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int Hkv, int d) {
+    if (T < 1 || keys < 1 || Hkv < 1 || Hq < 1 || d < 1) return 0;
+    return kv8_workspace(T, keys, Hq, Hkv, d);
+}
+
+dsa_status_t dsa_sparse_attn_kv8(const void* Q, const void* K8, const void* V8,
+                                 const float* k_scale, const float* v_scale, int64_t num_pages,
+                                 int page, const int32_t* block_table, int max_pages,
+                                 const int32_t* seq_lens, const int32_t* row_off, int B, int64_t T,
+                                 const int32_t* idx, int k, int Hq, int Hkv, int d, float scale,
+                                 void* O, float* lse, void* workspace, size_t workspace_bytes,
+                                 int32_t* err, dsa_stream_t stream) {
+    return run_attn_kv8("dsa_sparse_attn_kv8", Q, K8, V8, k_scale, v_scale, num_pages, page,
+                        block_table, max_pages, seq_lens, row_off, B, T, true, idx, k, Hq, Hkv, d,
+                        scale, O, lse, workspace, workspace_bytes, err, stream);
+}
+
+dsa_status_t dsa_attn_kv8(const void* Q, const void* K8, const void* V8, const float* k_scale,
+                          const float* v_scale, int64_t num_pages, int page,
+                          const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                          const int32_t* row_off, int B, int64_t T, int Hq, int Hkv, int d,
+                          float scale, void* O, float* lse, void* workspace,
+                          size_t workspace_bytes, int32_t* err, dsa_stream_t stream) {
+    return run_attn_kv8("dsa_attn_kv8", Q, K8, V8, k_scale, v_scale, num_pages, page, block_table,
+                        max_pages, seq_lens, row_off, B, T, false, nullptr, 0, Hq, Hkv, d, scale, O,
+                        lse, workspace, workspace_bytes, err, stream);
 }
 
 }  // extern "C"

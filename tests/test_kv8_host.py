@@ -111,3 +111,61 @@ def test_binding_checks_of_the_cache(change, match):
     x = torch.zeros((2, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match=match):
         dsa.kv8_append(x, x, **{**_cache(), **change})
+
+
+# Q, K8, V8, k_scale, v_scale, num_pages, page, block_table, max_pages, seq_lens, row_off, B, T
+CACHE = [FAKE, FAKE, FAKE, FAKE, FAKE, 10, 64, FAKE, 4, FAKE, FAKE, 3, 8]
+# Hq, Hkv, d, scale, O, lse, workspace, bytes, err, stream
+REST = [32, 4, 128, 0.1, FAKE, FAKE, FAKE, 1 << 30, None, None]
+SPARSE, DENSE = CACHE + [FAKE, 64] + REST, CACHE + REST
+
+
+@pytest.mark.parametrize("at,value,status", [
+    (0, None, INVALID), (0, FAKE + 8, INVALID), (1, None, INVALID), (2, FAKE + 4, INVALID),
+    (3, None, INVALID), (4, FAKE + 1, INVALID), (5, 0, INVALID), (5, 1 << 25, INVALID),
+    (6, 8, UNSUPPORTED), (6, 65, UNSUPPORTED), (7, None, INVALID), (8, 0, INVALID),
+    (8, 1 << 25, INVALID), (9, None, INVALID), (10, None, INVALID), (10, FAKE + 2, INVALID),
+    (11, 0, INVALID), (11, -3, INVALID), (11, 1 << 25, INVALID), (12, -1, INVALID),
+    (12, 1 << 30, UNSUPPORTED), (13, None, INVALID), (13, FAKE + 3, INVALID), (14, 0, INVALID),
+    (14, 65537, INVALID), (15, 30, INVALID), (15, 64, UNSUPPORTED), (15, 0, INVALID),
+    (16, 0, INVALID), (16, 128, INVALID), (17, 96, UNSUPPORTED), (18, 0.0, INVALID),
+    (18, -1.0, INVALID), (18, float("nan"), INVALID), (18, float("inf"), INVALID),
+    (19, None, INVALID), (20, FAKE + 2, INVALID), (21, None, INVALID), (21, FAKE + 8, INVALID),
+    (22, 15, WORKSPACE), (23, FAKE + 1, INVALID)])
+def test_attention_refusals(L, at, value, status):
+    a = list(SPARSE)
+    a[8], a[14] = 64, 2048  # sizes that need a workspace
+    assert L.dsa_attn_kv8_workspace_size(8, 2048, 32, 4, 128) > 15
+    a[at] = value
+    assert L.dsa_sparse_attn_kv8(*a) == status
+    assert b"dsa_sparse_attn_kv8" in L.dsa_last_error()
+    if at not in (13, 14):
+        assert L.dsa_attn_kv8(*a[:13], *a[15:]) == status
+        assert b"dsa_attn_kv8" in L.dsa_last_error()
+
+
+def test_attention_of_nothing(L):
+    a = list(SPARSE)
+    a[12] = 0
+    assert L.dsa_sparse_attn_kv8(*a) == OK
+    a = list(DENSE)
+    a[12] = 0
+    assert L.dsa_attn_kv8(*a) == OK
+
+
+def test_attention_workspace_sizes(L):
+    f = L.dsa_attn_kv8_workspace_size
+    assert f(0, 100, 32, 4, 128) == 0 and f(4, 0, 32, 4, 128) == 0
+    assert f(4, 100, 32, 0, 128) == 0 and f(-1, 100, 32, 4, 128) == 0
+    assert 0 < f(1, 1 << 20, 32, 4, 128) < 1 << 28
+    assert f(64, 2048, 32, 4, 128) < 1 << 28 and f(1 << 20, 2048, 32, 4, 128) < 1 << 30
+
+
+def test_binding_checks_of_the_attention():
+    c = _cache()
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    args = (c["k8"], c["v8"], c["k_scale"], c["v_scale"], c["block_table"], c["seq_lens"])
+    with pytest.raises(ValueError, match="CUDA"):
+        dsa.attn_kv8(q, *args, 0.1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        dsa.attn_kv8(q, *args[:5], torch.zeros(1, dtype=torch.int32), 0.1)
