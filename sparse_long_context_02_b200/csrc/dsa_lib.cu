@@ -1386,11 +1386,31 @@ int type_bytes(int type) {
 
 template <typename TI, typename TO>
 dsa_status_t launch_rope(const char* fn, dsa::rope::Params p, cudaStream_t st) {
-    // tokens per CTA: 2 while that leaves a CTA for every SM
-    p.tokens = p.L >= 2 * num_sms() ? 2 : 1;
+    bool vec = p.d % 16 == 0 && p.off % 16 == 0 && p.rot % 16 == 0;
+    for (int w = 0; w < 2; ++w)
+        if (p.H[w] > 0)
+            vec = vec && aligned16(p.x[w]) && aligned16(p.y[w]) &&
+                  p.xs[w] * (int64_t)sizeof(TI) % 16 == 0 && p.ys[w] * (int64_t)sizeof(TO) % 8 == 0 &&
+                  (sizeof(TO) == 1 || p.ys[w] * (int64_t)sizeof(TO) % 16 == 0);
+    // tokens per CTA: enough rows for a few rounds of every thread, while four
+    // CTAs per SM are left and the angles fit in 32 KB
+    const int64_t row = ((int64_t)(p.H[0] + p.H[1]) * p.d + 15) / 16;
+    int64_t n = p.L / (4 * num_sms());
+    const int64_t most = 2304 / row, fit = 32768 / (p.rot * 4);
+    n = n < most ? n : most;
+    n = n < fit ? n : fit;
+    n = n < 16 ? n : 16;
+    p.tokens = (int)(n < 1 ? 1 : n);
     const int64_t grid = (p.L + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * (p.rot / 2) * sizeof(float2);
-    dsa::rope::rope_kernel<TI, TO><<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
+    if (!vec)
+        dsa::rope::rope_kernel<TI, TO><<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
+    else if (p.interleaved)
+        dsa::rope::rope_vec_kernel<TI, TO, true>
+            <<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
+    else
+        dsa::rope::rope_vec_kernel<TI, TO, false>
+            <<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
     CUDA_TRY(cudaGetLastError());
     return ok();
 }

@@ -77,6 +77,7 @@ __device__ __forceinline__ float2 angle(const Params& p, int64_t t, int i) {
     return make_float2(c * p.rot_scale, p.inverse ? -s * p.rot_scale : s * p.rot_scale);
 }
 
+// Any alignment, any even sizes: one pair per thread and step.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     extern __shared__ float2 cs[];  // [tokens][rot / 2]
@@ -111,6 +112,143 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         }
         y[a] = from_f32<TO>(u * p.out_scale);
         y[b] = from_f32<TO>(v * p.out_scale);
+    }
+}
+
+// Eight consecutive elements, in 16-byte pieces (8 for e4m3).
+__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p) {
+    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + j);
+        v[4 * j] = q.x; v[4 * j + 1] = q.y; v[4 * j + 2] = q.z; v[4 * j + 3] = q.w;
+    }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        reinterpret_cast<float4*>(p)[j] =
+            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+
+__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float (&v)[8]) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w[j >> 2] |= (uint32_t)from_f32<__nv_fp8_e4m3>(v[j]).__x << (8 * (j & 3));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+// Heads of 16-element units (d, off and rot multiples of 16, 16-byte aligned
+// rows): a thread keeps one unit u of the head, two pieces of 8 elements, and
+// walks over (token, head) rows, two at a time so that four (fp32: eight)
+// 16-byte loads are in flight.  Units [0, rot / 16) hold 8 pairs each (pieces at
+// off + 8 u and off + rot / 2 + 8 u, or 16 u and 16 u + 8), the others pass through.
+// The (cos, sin) of a token's pairs lie as [2 pairs of the unit][unit], so that
+// the 8 threads of a 128-byte shared access read neighbours.
+template <typename TI, typename TO, bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
+    extern __shared__ float4 cs4[];  // [tokens][4][rot / 16]
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+    const int nt = (int)(p.L - t0 < p.tokens ? p.L - t0 : p.tokens);
+    const int half = p.rot / 2, ru = p.rot / 16;
+    for (int e = threadIdx.x; e < nt * half; e += kThreads) {
+        const int t = e / half, i = e % half;
+        reinterpret_cast<float2*>(cs4)[((t * 4 + (i & 7) / 2) * ru + (i >> 3)) * 2 + (i & 1)] =
+            angle(p, t0 + t, i);
+    }
+    __syncthreads();
+    const int units = p.d / 16, per = kThreads / units, H = p.H[0] + p.H[1];
+    const int u = threadIdx.x % units;
+    if ((int)threadIdx.x >= per * units) return;
+    int ea, eb;
+    if (u < ru) {
+        ea = p.off + (INTER ? 16 * u : 8 * u);
+        eb = ea + (INTER ? 8 : half);
+    } else {
+        ea = 16 * (u - ru);
+        if (ea >= p.off) ea += p.rot;
+        eb = ea + 8;
+    }
+    auto in = [&](int t, int h) {
+        const int w = h >= p.H[0];
+        return static_cast<const TI*>(p.x[w]) + (t0 + t) * p.xs[w] +
+               (int64_t)(w ? h - p.H[0] : h) * p.d;
+    };
+    auto turn = [&](int t, int h, float (&a)[8], float (&b)[8]) {
+        if (u < ru) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 c = cs4[(t * 4 + j) * ru + u];
+                float& a0 = INTER ? (j < 2 ? a[4 * j] : b[4 * j - 8]) : a[2 * j];
+                float& b0 = INTER ? (j < 2 ? a[4 * j + 1] : b[4 * j - 7]) : b[2 * j];
+                float& a1 = INTER ? (j < 2 ? a[4 * j + 2] : b[4 * j - 6]) : a[2 * j + 1];
+                float& b1 = INTER ? (j < 2 ? a[4 * j + 3] : b[4 * j - 5]) : b[2 * j + 1];
+                const float r0 = a0 * c.x - b0 * c.y, r1 = a1 * c.z - b1 * c.w;
+                b0 = b0 * c.x + a0 * c.y;
+                b1 = b1 * c.z + a1 * c.w;
+                a0 = r0;
+                a1 = r1;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[j] *= p.out_scale;
+            b[j] *= p.out_scale;
+        }
+        const int w = h >= p.H[0];
+        TO* y = static_cast<TO*>(p.y[w]) + (t0 + t) * p.ys[w] + (int64_t)(w ? h - p.H[0] : h) * p.d;
+        store8(y + ea, a);
+        store8(y + eb, b);
+    };
+    int t = 0, h = threadIdx.x / units;
+    auto next = [&] {
+        h += per;
+        while (h >= H) {
+            h -= H;
+            ++t;
+        }
+    };
+    h -= per;
+    next();
+    while (t < nt) {
+        float a0[8], b0[8], a1[8], b1[8];
+        const int tt = t, hh = h;
+        const TI* x = in(t, h);
+        load8(a0, x + ea);
+        load8(b0, x + eb);
+        next();
+        const bool two = t < nt;
+        if (two) {
+            x = in(t, h);
+            load8(a1, x + ea);
+            load8(b1, x + eb);
+        }
+        turn(tt, hh, a0, b0);
+        if (two) {
+            turn(t, h, a1, b1);
+            next();
+        }
     }
 }
 
