@@ -1570,35 +1570,77 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
     return launch_append<128, D>(fn, p, units, st);
 }
 
-// Slices per row: enough CTAs for two per resident slot (four of 128 threads
-// per SM), none shorter than 64 keys.
-int kv8_splits(int64_t T, int64_t cap, int Hkv) {
-    const int64_t want = (int64_t)num_sms() * 8 / (T * Hkv);
-    const int64_t most = (cap + 63) / 64;
-    const int64_t n = want < most ? want : most;
-    return (int)(n < 1 ? 1 : n > 256 ? 256 : n);
+// How a launch divides: KV heads per CTA, CTAs per group of heads, bytes of the
+// partial results.  One CTA per SM in all, and none with fewer than two units.
+struct Kv8Plan {
+    int hg, ctas;
+    size_t part_o, part_m, total;
+};
+
+Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
+    Kv8Plan pl{};
+    pl.hg = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+    const int64_t most = num_sms() / (Hkv / pl.hg);
+    const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;
+    const int64_t want = T > (int64_t(1) << 40) / per ? most : T * per / 2;
+    pl.ctas = (int)(want < 1 ? 1 : want < most ? want : most);
+    if (pl.ctas > 1) {
+        pl.part_o = align256((size_t)pl.ctas * 2 * Hq * d * 4);
+        pl.part_m = align256((size_t)pl.ctas * 2 * Hq * 16);
+        pl.total = pl.part_o + pl.part_m + align256((size_t)pl.ctas * 16);
+    }
+    return pl;
 }
 
-size_t kv8_workspace(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
-    const int ns = kv8_splits(T, cap, Hkv);
-    return ns == 1 ? 0 : align256((size_t)T * ns * Hq * d * 4) + align256((size_t)T * ns * Hq * 16);
+// [positions][Hkv][d] bytes with boxes of one head and box_rows positions,
+// swizzled as make_map's.
+bool make_pool_map(CUtensorMap* m, const void* base, int d, int Hkv, int64_t positions,
+                   int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)Hkv, (cuuint64_t)positions};
+    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * Hkv};
+    cuuint32_t box[3] = {(cuuint32_t)d, 1, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, cudaStream_t st) {
-    const dim3 grid((unsigned)(p.rows.n * p.Hkv), (unsigned)p.nsplit);
-    if (p.idx != nullptr)
-        dsa::kv8::attn_kernel<D, false><<<grid, dsa::kv8::kWarps * 32, 0, st>>>(p);
-    else
-        dsa::kv8::attn_kernel<D, true><<<grid, dsa::kv8::kWarps * 32, 0, st>>>(p);
+template <int D, int HG, bool DENSE>
+dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int ctas, bool merge,
+                             cudaStream_t st) {
+    namespace kv = dsa::kv8;
+    using C = kv::AttnCfg<D, HG>;
+    auto kern = kv::attn_kernel<D, HG, DENSE>;
+    CUtensorMap maps[2] = {};
+    if (DENSE) {
+        const int page = 1 << p.page_log2, rows = page < kv::kKeys ? page : kv::kKeys;
+        for (int w = 0; w < 2; ++w)
+            if (!make_pool_map(&maps[w], p.code[w], D, p.Hkv, p.pages * page, rows))
+                return fail(DSA_ERR_CUDA, "%s: tensor map", fn);
+    }
+    CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    kern<<<dim3((unsigned)ctas, (unsigned)(p.Hkv / HG)), kv::kAttnThreads, C::SMEM, st>>>(
+        p, maps[0], maps[1]);
     CUDA_TRY(cudaGetLastError());
-    if (p.nsplit > 1) {
-        CUDA_TRY(launch_chained(dsa::kv8::combine_kernel<D>,
-                                dim3((unsigned)(p.Hkv * p.G), (unsigned)p.rows.n), dim3(D), 0, st,
-                                p));
+    if (merge) {
+        const int64_t n = p.rows.n < ctas ? p.rows.n : ctas;
+        CUDA_TRY(launch_chained(kv::combine_kernel<D>, dim3((unsigned)n, (unsigned)(p.Hkv * p.G)),
+                                dim3(D), 0, st, p));
         CUDA_TRY(cudaGetLastError());
     }
     return ok();
+}
+
+template <int D, bool DENSE>
+dsa_status_t dispatch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, const Kv8Plan& pl,
+                               bool merge, cudaStream_t st) {
+    if (pl.hg == 4) return launch_kv8_attn<D, 4, DENSE>(fn, p, pl.ctas, merge, st);
+    if (pl.hg == 2) return launch_kv8_attn<D, 2, DENSE>(fn, p, pl.ctas, merge, st);
+    return launch_kv8_attn<D, 1, DENSE>(fn, p, pl.ctas, merge, st);
 }
 
 dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const void* V8,
@@ -1638,11 +1680,12 @@ dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const v
     CHECK_PTR(O);
     if (lse != nullptr) CHECK_PTR4(lse);
     const int64_t cap = sparse ? k : (int64_t)max_pages * page;
-    const size_t need = kv8_workspace(T, cap, Hq, Hkv, d);
-    if (need > 0) {
+    const Kv8Plan pl = kv8_plan(T, cap, Hq, Hkv, d);
+    if (pl.total > 0) {
         CHECK_PTR(workspace);
-        if (workspace_bytes < need)
-            return fail(DSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+        if (workspace_bytes < pl.total)
+            return fail(DSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
+                        pl.total);
     }
     dsa::kv8::AttnParams p{};
     p.Q = static_cast<const __nv_bfloat16*>(Q);
@@ -1661,15 +1704,24 @@ dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const v
     p.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     p.pages = num_pages;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.nsplit = kv8_splits(T, cap, Hkv);
+    p.vec_scales = aligned16(k_scale) && aligned16(v_scale);
+    p.whole_rows = !sparse && T > dsa::kv8::kMaxScan;
     p.O = static_cast<__nv_bfloat16*>(O);
     p.lse = lse;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_m = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                        align256((size_t)T * p.nsplit * Hq * d * 4));
+    const bool merge = pl.ctas > 1 && !p.whole_rows;
+    if (merge) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.part_o = reinterpret_cast<float*>(ws);
+        p.part_m = reinterpret_cast<float*>(ws + pl.part_o);
+        p.part_row = reinterpret_cast<int4*>(ws + pl.part_o + pl.part_m);
+    }
     p.err = err;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return d == 128 ? launch_kv8_attn<128>(fn, p, st) : launch_kv8_attn<64>(fn, p, st);
+    if (sparse)
+        return d == 128 ? dispatch_kv8_attn<128, false>(fn, p, pl, merge, st)
+                        : dispatch_kv8_attn<64, false>(fn, p, pl, merge, st);
+    return d == 128 ? dispatch_kv8_attn<128, true>(fn, p, pl, merge, st)
+                    : dispatch_kv8_attn<64, true>(fn, p, pl, merge, st);
 }
 
 }  // namespace
@@ -1735,8 +1787,8 @@ dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int64_t k_s
 }
 
 size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int Hkv, int d) {
-    if (T < 1 || keys < 1 || Hkv < 1 || Hq < 1 || d < 1) return 0;
-    return kv8_workspace(T, keys, Hq, Hkv, d);
+    if (T < 1 || keys < 1 || Hkv < 1 || Hq < 1 || d < 1 || Hkv > 64 || Hq > 1024 || d > 1024) return 0;
+    return kv8_plan(T, keys, Hq, Hkv, d).total;
 }
 
 dsa_status_t dsa_sparse_attn_kv8(const void* Q, const void* K8, const void* V8,

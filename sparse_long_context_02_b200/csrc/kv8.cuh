@@ -218,16 +218,46 @@ struct AttnParams {
     const int32_t* idx;          // [T][k], or null: every key
     Rows rows;
     int M, Hkv, G, k, page_log2;
+    int vec_scales;              // a group's scales may be read as one vector
     int64_t pages;
     float scale_log2;            // softmax scale * log2(e)
-    int nsplit;                  // slices of a row's keys
+    int whole_rows;              // every key: rows are dealt out whole
     __nv_bfloat16* O;            // [T][Hq][d]
     float* lse;                  // [T][Hq] or null
-    // With nsplit > 1, per (row, slice, head): sums of 2^(y - My) V, and
-    // (Mx, My, l), see attn_kernel.
-    float* part_o;               // [T][nsplit][Hq][d]
-    float* part_m;               // [T][nsplit][Hq][4]
+    // Rows that several CTAs share, per (CTA, its first or its last row, head): sums of
+    // 2^(y - My + 15) V, and (Mx, My, l), see attn_kernel; per CTA which rows these are.
+    float* part_o;               // [C][2][Hq][d]
+    float* part_m;               // [C][2][Hq][4]
+    int4* part_row;              // [min(T, C)], null: no row is shared
     int* err;
+};
+
+constexpr int kConsumers = 8;    // consumer warps
+constexpr int kProducers = 4;    // producer warps
+constexpr int kAttnThreads = (kConsumers + kProducers) * 32;
+constexpr int kKeys = 32;        // keys of one unit: a stage of the ring
+constexpr int kMaxScan = 512;    // rows whose lengths a CTA adds up itself
+constexpr float kWeightLog2 = 15.f;                // the largest fp16 weight is 2^15
+constexpr float kWeightScale = 3.0517578125e-05f;  // 2^-15
+
+template <int D, int HG>
+struct AttnCfg {
+    static constexpr int NSUB = kConsumers / HG;        // warps that take turns at a head's units
+    static constexpr int BOX = kKeys * D;               // one head's K (or V) codes of a unit
+    static constexpr int STAGE = 2 * HG * BOX;
+    static constexpr int FIT = 4 * 32768 / STAGE;
+    static constexpr int STAGES = FIT < 16 ? FIT : 16;
+    // A stage always belongs to the same producer warp and the same consumers: a barrier's
+    // parity only tells neighbouring phases apart, so whoever waits for a phase has to have
+    // waited for (or caused) the one before it.
+    static_assert(STAGES % kProducers == 0 && STAGES % NSUB == 0, "");
+    static constexpr int OROW = D + 4;
+    static constexpr int O_AT = STAGES * STAGE;
+    static constexpr int SC_AT = O_AT + kConsumers * 8 * OROW * 4;
+    static constexpr int M_AT = SC_AT + STAGES * HG * kKeys * 8;
+    static constexpr int SCAN_AT = M_AT + kConsumers * 8 * 16;
+    static constexpr int BAR_AT = SCAN_AT + (kMaxScan + 2) * 8;
+    static constexpr int SMEM = BAR_AT + STAGES * 20;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -236,15 +266,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-constexpr int kWarps = 4;
-constexpr float kWeightLog2 = 15.f;  // the largest fp16 weight is 2^15
-constexpr float kWeightScale = 3.0517578125e-05f;  // 2^-15
-constexpr int kChunk = 512;      // keys whose places and scales are staged at once
-
 // The sequence of row t and the number of keys it sees; false: the row belongs
 // to no sequence (it lies behind the last one).
-__device__ __forceinline__ bool find_row(const AttnParams& p, int64_t t, int& b, int64_t& n) {
+__device__ __forceinline__ bool find_row(const AttnParams& p, int64_t t, bool report, int& b,
+                                         int64_t& n) {
     const Rows& rw = p.rows;
+    b = 0;
+    n = 0;
     if (rw.off == nullptr) {
         b = (int)t;
         n = p.lens[b];
@@ -260,7 +288,7 @@ __device__ __forceinline__ bool find_row(const AttnParams& p, int64_t t, int& b,
         n = p.lens[b];
         const int64_t later = (int64_t)rw.off[b + 1] - 1 - t;
         if (later < 0 || rw.off[b + 1] > rw.n) {  // offsets that do not ascend
-            if (threadIdx.x == 0) record_error_to(p.err, 2);
+            if (report) record_error_to(p.err, 2);
             n = 0;
         }
         // rows of a sequence are its last tokens; over every key they are causal
@@ -268,11 +296,18 @@ __device__ __forceinline__ bool find_row(const AttnParams& p, int64_t t, int& b,
     }
     const int64_t cap = (int64_t)p.M << p.page_log2;
     if (n > cap) {
-        if (threadIdx.x == 0) record_error_to(p.err, 2);
+        if (report) record_error_to(p.err, 2);
         n = cap;
     }
     if (n < 0) n = 0;
     return true;
+}
+
+__device__ __forceinline__ int64_t row_units(const AttnParams& p, int64_t t) {
+    int b;
+    int64_t n;
+    find_row(p, t, false, b, n);
+    return n <= kKeys ? 1 : (n + kKeys - 1) / kKeys;  // a row without keys has a unit, too
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -297,34 +332,105 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ void load_codes(uint32_t (&r)[N], const uint8_t* q, bool ok) {
-    static_assert(N == 4 || N == 2, "");
-    if constexpr (N == 4) {
-        const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(q)) : make_uint4(0, 0, 0, 0);
-        r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-    } else {
-        const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(q)) : make_uint2(0, 0);
-        r[0] = v.x; r[1] = v.y;
-    }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
 }
 
-// One CTA per (KV head, slice, row).  Each warp takes every kWarps-th tile of 16
-// keys by itself: no barrier inside a chunk, one merge at the end.
+// The rows and units of one CTA, in order.  The units of all rows, laid end to
+// end, are cut into equal ranges, one per CTA (whole_rows: CTA c takes the rows
+// c, c + C, ...).  Every warp walks by itself.
+struct Walk {
+    int64_t t;           // row
+    int64_t a, b, all;   // this CTA's units [a, b) of the row's [0, all)
+    int64_t left;        // units of later rows
+    int64_t U, C;        // all units, and the CTAs that share them
+
+    template <bool DENSE>
+    __device__ __forceinline__ void open(const AttnParams& p, const int64_t* scan) {
+        if (DENSE && p.whole_rows) {
+            t = blockIdx.x;
+            a = 0;
+            b = all = t < p.rows.n ? row_units(p, t) : 0;
+            left = 0;
+            return;
+        }
+        const int64_t per = (p.k + kKeys - 1) / kKeys;
+        U = DENSE ? scan[p.rows.n] : p.rows.n * per;
+        C = U < gridDim.x ? U : gridDim.x;  // CTAs behind the last unit have none
+        const int64_t c = blockIdx.x < C ? blockIdx.x : C;
+        const int64_t u0 = U * c / C, u1 = c < C ? U * (c + 1) / C : U;
+        if (DENSE) {
+            int lo = 0, hi = (int)p.rows.n - 1;  // the last row that starts at u0 or before
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (scan[mid] <= u0) lo = mid;
+                else hi = mid - 1;
+            }
+            t = lo;
+            all = scan[lo + 1] - scan[lo];
+            a = u0 - scan[lo];
+        } else {
+            t = u0 / per;
+            all = per;
+            a = u0 - t * per;
+        }
+        left = u1 - u0;
+        b = a + left < all ? a + left : all;
+        left -= b - a;
+    }
+
+    __device__ __forceinline__ bool done() const { return a >= b; }
+
+    template <bool DENSE>
+    __device__ __forceinline__ void next(const AttnParams& p, const int64_t* scan) {
+        a = 0;
+        if (DENSE && p.whole_rows) {
+            t += gridDim.x;
+            b = all = t < p.rows.n ? row_units(p, t) : 0;
+            return;
+        }
+        ++t;
+        if (left == 0) {
+            b = 0;
+            return;
+        }
+        if (DENSE) all = scan[t + 1] - scan[t];
+        b = left < all ? left : all;
+        left -= b;
+    }
+};
+
+// Attention of rows over cached keys.  A CTA serves HG neighbouring KV heads of
+// its range of units (32 keys of one row): four producer warps bring units into
+// a ring of shared-memory stages, eight consumer warps compute, HG of them, one
+// per head, at each unit, the others at the units between.
 //
-// S^T = K Q^T: the 16 keys are the rows of an m16n8k16 product, the head
-// group's queries (up to 8) its columns.  The sum over d may run in any order,
-// so thread (g, t) of the quad layout takes d = 16 t .. 16 t + 15 of keys g and
-// g + 8 straight from global memory as one 16-byte load, which feeds four
-// products; Q is laid out to match, once.  K is exact in fp16; Q's bf16 is made
-// exact in fp16 by a power of two per head that puts its largest element at
-// 2^14 (what falls below 2^-24 there is under 2^-38 of that element).
+// Copies.  Selected keys are gathered with 16-byte cp.async, a warp taking a
+// key's HG * d bytes at once (rows this short are too many for the copy
+// engine); over every key a unit lies inside a page and comes as one TMA box
+// per head.  Either way a head's 32 rows of d bytes lie with their 16-byte
+// pieces exclusive-or'ed by the row, as TMA's swizzle does.
+//
+// S^T = K Q^T: 16 keys are the rows of an m16n8k16 product, the head group's
+// queries (up to 8) its columns.  The sum over d may run in any order, so thread
+// (g, t) of the quad layout takes d = 16 t .. 16 t + 15 of its two keys as one
+// 16-byte read, which feeds four products; Q is laid out to match, once per row.
+// K is exact in fp16; Q's bf16 is made exact in fp16 by a power of two per head
+// that puts its largest element at 2^14 (what falls below 2^-24 there is under
+// 2^-38 of that element).
 //
 // O^T += V^T P: the rows are d, the columns heads, the depth the 16 keys.
-// Thread (g, t) needs keys 2t, 2t+1, 2t+8, 2t+9 at its d, again 16 contiguous
-// bytes of each key; byte permutes pair two keys' codes before widening.  The
-// score tile's (key, head) fragment becomes the (head, key) operand by an 8x8
-// transpose in registers.
+// Thread (g, t) needs four keys at its d, again 16 contiguous bytes of each key;
+// byte permutes pair two keys' codes before widening.  The score tile's (key,
+// head) fragment becomes the (head, key) operand by an 8x8 transpose in
+// registers.  Which key stands at which place of a tile is free: `place` orders
+// them so that the eight threads of a shared access meet eight different
+// 16-byte columns, for K (two keys x 64 bytes) and for V (four keys x 32).
 //
 // Softmax in log2 units: x = score, y = x + log2(v_scale[key]).  Two running
 // maxima are kept: Mx for l = sum 2^(x - Mx), My for the weights 2^(y - My) that
@@ -333,251 +439,478 @@ __device__ __forceinline__ void load_codes(uint32_t (&r)[N], const uint8_t* q, b
 // rounding them costs 2^-11 each, an eighth of the output's own bf16 rounding,
 // down to 2^-29 of the largest, and 2^-40 of it below, so that a long tail of
 // small weights (2^18 keys and more) still counts.
-template <int D, bool DENSE>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(const AttnParams p) {
-    constexpr int NL = D / 64;       // 16-byte loads per key row and quad thread
+template <int D, int HG, bool DENSE>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
+            const __grid_constant__ CUtensorMap mv) {
+    using C = AttnCfg<D, HG>;
+    constexpr int NL = D / 64;       // 16-byte reads per key row and quad thread
     constexpr int MT = D / 16;       // m16 tiles of d
     constexpr int VW = D / 32;       // 32-bit words of one key's V row per thread
-    const int h = blockIdx.x % p.Hkv, sp = blockIdx.y;
-    const int64_t t = blockIdx.x / p.Hkv;
+    pdl_launch_dependents();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float* o_s = reinterpret_cast<float*>(smem + C::O_AT);       // [warp][8][OROW]
+    float2* sc_s = reinterpret_cast<float2*>(smem + C::SC_AT);   // [stage][HG][32]: k scale, log2 v
+    float4* m_s = reinterpret_cast<float4*>(smem + C::M_AT);     // [warp][8]: Mx, My, l
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + C::SCAN_AT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_AT);
+    uint64_t* empty = full + C::STAGES;
+    uint32_t* mask_s = reinterpret_cast<uint32_t*>(empty + C::STAGES);
+
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t4 = lane & 3;
-    const int PAGE = 1 << p.page_log2;
-
-    __shared__ int32_t row_s[kChunk];      // page * PAGE + slot, -1: no key
-    __shared__ float ks_s[kChunk];         // k scale
-    __shared__ float lv_s[kChunk];         // log2 of the v scale
-    __shared__ float o_s[kWarps][8][D + 4];
-    __shared__ float m_s[kWarps][8][3];    // Mx, My, l
-
-    int b;
-    int64_t n;
-    if (!find_row(p, t, b, n)) return;
-    // this slice's entries (list positions, or keys)
-    const int64_t total = DENSE ? n : p.k;
-    const int64_t per = ((total + p.nsplit - 1) / p.nsplit + 15) / 16 * 16;
-    const int64_t e0 = sp * per < total ? sp * per : total;
-    const int64_t e1 = e0 + per < total ? e0 + per : total;
-
-    // Q, scaled by 2^qe
-    uint32_t qf[NL][4][2];
-    float qs[2];                           // for heads 2 t4, 2 t4 + 1
-    {
-        const __nv_bfloat16* q = p.Q + (t * p.Hkv * p.G + (int64_t)h * p.G + g) * D;
-        uint32_t raw[NL][8];
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            uint4 a = make_uint4(0, 0, 0, 0), c = a;
-            if (g < p.G) {
-                a = *reinterpret_cast<const uint4*>(q + 64 * i + 16 * t4);
-                c = *reinterpret_cast<const uint4*>(q + 64 * i + 16 * t4 + 8);
-            }
-            raw[i][0] = a.x; raw[i][1] = a.y; raw[i][2] = a.z; raw[i][3] = a.w;
-            raw[i][4] = c.x; raw[i][5] = c.y; raw[i][6] = c.z; raw[i][7] = c.w;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                top = max(top, max(raw[i][j] & 0x7fffu, raw[i][j] >> 16 & 0x7fffu));
+    const int h0 = blockIdx.y * HG;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), DENSE ? 1 : 33);
+            mbar_init(smem_u32(&empty[s]), HG);
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the exponent that brings the largest element to [2^14, 2^15)
-        int qe = top == 0 || top >= 0x7f80u ? 0 : 14 + 127 - (int)max(top >> 7, 1u);
-        qe = min(qe, 126);
-        const float up = __uint_as_float((uint32_t)(qe + 127) << 23);
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const __half2 v = __floats2half2_rn(__uint_as_float(raw[i][j] << 16) * up,
-                                                    __uint_as_float(raw[i][j] & 0xffff0000u) * up);
-                qf[i][j >> 1][j & 1] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-        const float back = p.scale_log2 * __uint_as_float((uint32_t)(127 - qe) << 23);
-        qs[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
-        qs[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
+        fence_mbar_init();
     }
-
-    float o[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    for (int64_t c0 = e0; c0 < e1; c0 += kChunk) {
-        const int cn = (int)(e1 - c0 < kChunk ? e1 - c0 : kChunk);
+    if (DENSE && !p.whole_rows) {
+        for (int t = threadIdx.x; t < p.rows.n; t += kAttnThreads) scan[t + 1] = row_units(p, t);
         __syncthreads();
-        for (int e = threadIdx.x; e < (cn + 15) / 16 * 16; e += kWarps * 32) {
-            int64_t key = -1;
-            if (e < cn) key = DENSE ? c0 + e : (int64_t)p.idx[t * p.k + c0 + e];
-            int32_t row = -1;
-            float ks = 0.f, lv = -INFINITY;
-            if (key >= 0) {
-                const int32_t pg = key < n ? p.table[(int64_t)b * p.M + (key >> p.page_log2)] : -1;
-                if (pg >= 0 && pg < p.pages) {
-                    row = (int32_t)(((int64_t)pg << p.page_log2) + (key & (PAGE - 1)));
-                    ks = p.scale[0][(int64_t)pg * p.Hkv + h];
-                    lv = log2f(p.scale[1][(int64_t)pg * p.Hkv + h]);
-                } else {
-                    record_error_to(p.err, 2);
+        if (warp == 0) {
+            int64_t base = 0;
+            for (int t0 = 0; t0 < p.rows.n; t0 += 32) {
+                int64_t v = t0 + lane < p.rows.n ? scan[t0 + lane + 1] : 0;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int64_t w = __shfl_up_sync(0xffffffffu, v, d);
+                    if (lane >= d) v += w;
                 }
+                if (t0 + lane < p.rows.n) scan[t0 + lane + 1] = base + v;
+                base += __shfl_sync(0xffffffffu, v, 31);
             }
-            row_s[e] = row;
-            ks_s[e] = ks;
-            lv_s[e] = lv;
-        }
-        __syncthreads();
-        for (int e = warp * 16; e < cn; e += kWarps * 16) {
-            const int64_t rb = (int64_t)p.Hkv * D;
-            const int32_t rk[2] = {row_s[e + g], row_s[e + g + 8]};
-            uint32_t kr[2][NL][4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < NL; ++i)
-                    load_codes<4>(kr[j][i], p.code[0] + rk[j] * rb + h * D + 64 * i + 16 * t4,
-                                  rk[j] >= 0);
-            uint32_t vr[4][VW];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int32_t rv = row_s[e + 2 * t4 + (j & 1) + (j >> 1) * 8];
-                load_codes<VW>(vr[j], p.code[1] + rv * rb + h * D + VW * 4 * g, rv >= 0);
-            }
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < NL; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a[4] = {widen(kr[0][i][j]), widen(kr[1][i][j]),
-                                           widen(kr[0][i][j] >> 16), widen(kr[1][i][j] >> 16)};
-                    mma_f16(s, a, qf[i][j][0], qf[i][j][1]);
-                }
-            // x, y of keys g and g + 8, heads 2 t4 and 2 t4 + 1
-            float x[4], y[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int kk = e + g + (j >> 1) * 8;
-                x[j] = rk[j >> 1] >= 0 ? s[j] * (ks_s[kk] * qs[j & 1]) : -INFINITY;
-                y[j] = x[j] + lv_s[kk];
-            }
-            float wgt[4];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float ax = fmaxf(x[c], x[c + 2]), ay = fmaxf(y[c], y[c + 2]);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    ax = fmaxf(ax, __shfl_xor_sync(0xffffffffu, ax, d));
-                    ay = fmaxf(ay, __shfl_xor_sync(0xffffffffu, ay, d));
-                }
-                const float nx = fmaxf(mx[c], ax), ny = fmaxf(my[c], ay);
-                const float ux = nx == -INFINITY ? 0.f : nx, uy = ny == -INFINITY ? 0.f : ny;
-                const float fx = ex2(mx[c] - ux), fy = ex2(my[c] - uy);
-                const float ry = uy - kWeightLog2;
-                mx[c] = nx;
-                my[c] = ny;
-                l[c] = l[c] * fx + ex2(x[c] - ux) + ex2(x[c + 2] - ux);
-                wgt[c] = ex2(y[c] - ry);
-                wgt[c + 2] = ex2(y[c + 2] - ry);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    o[i][c] *= fy;
-                    o[i][c + 2] *= fy;
-                }
-            }
-            uint32_t pf[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const __half2 v = __floats2half2_rn(wgt[2 * j], wgt[2 * j + 1]);
-                pf[j] = transpose8x8(*reinterpret_cast<const uint32_t*>(&v));
-            }
-#pragma unroll
-            for (int i = 0; i < VW; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t sel = j ? 0x7362u : 0x5140u;
-                    const uint32_t lo = __byte_perm(vr[0][i], vr[1][i], sel);
-                    const uint32_t hi = __byte_perm(vr[2][i], vr[3][i], sel);
-                    const uint32_t a[4] = {widen(lo), widen(lo >> 16), widen(hi), widen(hi >> 16)};
-                    mma_f16(o[2 * i + j], a, pf[0], pf[1]);
-                }
-        }
-    }
-
-    // ---- the warps' partial results
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int hh = 2 * t4 + c;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {  // m tile i, rows g and g + 8: d = MT * 2 * g + 2 i, + 1
-            o_s[warp][hh][2 * MT * g + 2 * i] = o[i][c];
-            o_s[warp][hh][2 * MT * g + 2 * i + 1] = o[i][c + 2];
-        }
-        if (g == 0) {
-            m_s[warp][hh][0] = mx[c];
-            m_s[warp][hh][1] = my[c];
-            m_s[warp][hh][2] = l[c];
+            if (lane == 0) scan[0] = 0;
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.G * D; e += kWarps * 32) {
-        const int hh = e / D, d = e % D;
-        float Mx = -INFINITY, My = -INFINITY;
+
+    Walk w;
+    w.open<DENSE>(p, scan);
+
+    if (warp >= kConsumers) {
+        // ------------------------------------------------ producers
+        const int pw = warp - kConsumers;
+        const int64_t rb = (int64_t)p.Hkv * D;
+        int i = pw;                    // this warp's units: pw, pw + kProducers, ...
+        int64_t u = w.a + pw;          // the unit inside row w.t
+        int issued = -1;
+        int64_t total = w.b - w.a;     // units of the rows so far
+        bool ok = true;
+        int64_t tb = -1, n = 0;        // row of the cached lookup, its sequence and keys
+        int b = 0;
+        // Advances to this warp's next unit; false at the end.
+        auto settle = [&] {
+            while (!w.done() && u >= w.b) {
+                u -= w.b;
+                w.next<DENSE>(p, scan);
+                total += w.b;
+            }
+            return !w.done();
+        };
+        auto entry = [&](int64_t t, int64_t unit) -> int64_t {
+            if (tb != t) {
+                tb = t;
+                if (!find_row(p, t, lane == 0, b, n)) n = -1;
+            }
+            const int64_t e = unit * kKeys + lane;
+            if (n < 0) return -1;
+            if (DENSE) return e < n ? e : -1;
+            return e < p.k ? (int64_t)__ldg(p.idx + t * p.k + e) : -1;
+        };
+        auto page_of = [&](int64_t key) -> int32_t {
+            if (key < 0) return -1;
+            const int32_t pg = key < n ? __ldg(p.table + (int64_t)b * p.M + (key >> p.page_log2)) : -1;
+            if (pg >= 0 && pg < p.pages) return pg;
+            record_error_to(p.err, 2);
+            return -1;
+        };
+        bool more = settle();
+        int64_t key = more ? entry(w.t, u) : -1;
+        int32_t pg = page_of(key);
+        while (more && ok) {
+            // this unit's scales, and the next unit's keys, are under way while its copies go out
+            float ks[HG], vs[HG];
+            {
+                const int64_t at = (int64_t)(pg < 0 ? 0 : pg) * p.Hkv + h0;
+                const float *a = p.scale[0] + at, *c = p.scale[1] + at;
+                if (HG == 4 && p.vec_scales) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(a));
+                    const float4 y = __ldg(reinterpret_cast<const float4*>(c));
+                    ks[0] = x.x; ks[1 % HG] = x.y; ks[2 % HG] = x.z; ks[3 % HG] = x.w;
+                    vs[0] = y.x; vs[1 % HG] = y.y; vs[2 % HG] = y.z; vs[3 % HG] = y.w;
+                } else {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            Mx = fmaxf(Mx, m_s[w][hh][0]);
-            My = fmaxf(My, m_s[w][hh][1]);
-        }
-        const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
-        float ls = 0.f, acc = 0.f;
+                    for (int h = 0; h < HG; ++h) {
+                        ks[h] = __ldg(a + h);
+                        vs[h] = __ldg(c + h);
+                    }
+                }
+            }
+            const int32_t slot = (int32_t)key & ((1 << p.page_log2) - 1);
+            const int32_t row = (int32_t)((uint32_t)pg << p.page_log2) + slot;  // below 2^31
+            const bool valid = pg >= 0;
+            u += kProducers;
+            more = settle();
+            const int64_t key2 = more ? entry(w.t, u) : -1;
+
+            const int s = i % C::STAGES;
+            if (i >= C::STAGES) {
+                bool got = false;
+                if (lane == 0)
+                    got = mbar_wait_to(p.err, smem_u32(&empty[s]), ((i / C::STAGES) - 1) & 1);
+                ok = __shfl_sync(0xffffffffu, got, 0);
+                if (!ok) break;
+            }
+            const uint32_t bal = __ballot_sync(0xffffffffu, valid);
+            const uint32_t base = smem_u32(smem + s * C::STAGE), fb = smem_u32(&full[s]);
+            if constexpr (!DENSE) {
+                if (bal) {
+                    constexpr int CPR = HG * D / 16;   // 16-byte pieces of a key's row
+                    constexpr int RPI = 32 / CPR;      // rows per instruction
+                    const int c = lane % CPR, r0 = lane / CPR;
+                    const int hh = c / (D / 16), cc = c % (D / 16);
+                    const int64_t off = (int64_t)h0 * D + c * 16;
+                    const uint8_t *kp = p.code[0] + off, *vp = p.code[1] + off;
+                    const uint32_t dst = base + hh * C::BOX;
+#pragma unroll 8
+                    for (int r = r0; r < kKeys; r += RPI) {
+                        const int64_t src = (int64_t)__shfl_sync(0xffffffffu, row, r) * rb;
+                        const int sw = D == 128 ? cc ^ (r & 7) : cc ^ (r >> 1 & 3);
+                        if (bal >> r & 1u) {
+                            cp_async16(dst + r * D + sw * 16, kp + src);
+                            cp_async16(dst + HG * C::BOX + r * D + sw * 16, vp + src);
+                        }
+                    }
+                }
+            }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            ls += m_s[w][hh][2] * ex2(m_s[w][hh][0] - ux);
-            acc += o_s[w][hh][d] * ex2(m_s[w][hh][1] - uy);
+            for (int h = 0; h < HG; ++h)
+                sc_s[(s * HG + h) * kKeys + lane] = make_float2(ks[h], __log2f(vs[h]));
+            if (lane == 0) mask_s[s] = bal;
+            __syncwarp();
+            if constexpr (DENSE) {
+                // one box per head and tensor, two where a page is half a unit
+                const int boxes = p.page_log2 < 5 ? 2 : 1, rows = kKeys / boxes;
+                const int32_t r1 = __shfl_sync(0xffffffffu, row, 16);
+                if (lane == 0) {
+                    const bool have[2] = {(bal & 1u) != 0, boxes == 2 && (bal >> 16 & 1u)};
+                    mbar_arrive_expect_tx(fb, (have[0] + have[1]) * 2 * HG * rows * D);
+                    for (int q = 0; q < boxes; ++q)
+                        if (have[q])
+#pragma unroll
+                            for (int h = 0; h < HG; ++h) {
+                                const uint32_t dst = base + h * C::BOX + q * rows * D;
+                                const int32_t z = q ? r1 : row;
+                                tma_load_3d(dst, &mk, fb, 0, h0 + h, z);
+                                tma_load_3d(dst + HG * C::BOX, &mv, fb, 0, h0 + h, z);
+                            }
+                }
+            } else {
+                cp_async_arrive(fb);
+                if (lane == 0) mbar_arrive(fb);
+            }
+            issued = i;
+            i += kProducers;
+            key = key2;
+            pg = page_of(key);
         }
-        const int64_t head = (int64_t)h * p.G + hh;
-        const int64_t Hq = (int64_t)p.Hkv * p.G;
-        if (p.nsplit == 1) {
-            p.O[(t * Hq + head) * D + d] =
-                __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
-            if (p.lse != nullptr && d == 0)
-                p.lse[t * Hq + head] = ls == 0.f ? -INFINITY
-                                                 : (Mx + log2f(ls)) * 0.6931471805599453f;
-        } else {
-            const int64_t at = (t * p.nsplit + sp) * Hq + head;
-            p.part_o[at * D + d] = acc;
-            if (d == 0)
-                *reinterpret_cast<float4*>(p.part_m + at * 4) = make_float4(Mx, My, ls, 0.f);
+        // copies in flight end before the CTA does (earlier units' stages were taken again)
+        if (lane == 0)
+            for (int j = issued; j >= 0 && j + C::STAGES >= total; j -= kProducers)
+                if (!mbar_wait_to(p.err, smem_u32(&full[j % C::STAGES]), (j / C::STAGES) & 1)) break;
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int h = warp % HG, sub = warp / HG;
+    const int g = lane >> 2, t4 = lane & 3;
+    auto place = [](int m) { return (int)((D == 128 ? 0x37156240u : 0x65742130u) >> (4 * m) & 7u); };
+    const int pk = place(g);
+    const uint32_t mine = smem_u32(smem) + h * C::BOX;
+    uint32_t koff[NL], voff[2];
+#pragma unroll
+    for (int i = 0; i < NL; ++i)
+        koff[i] = pk * D + (D == 128 ? (4 * i + t4) ^ pk : t4 ^ (pk >> 1)) * 16;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = place(2 * t4 + e);
+        voff[e] = HG * C::BOX + r * D +
+                  (D == 128 ? (g ^ r) * 16 : ((g >> 1) ^ (r >> 1)) * 16 + (g & 1) * 8);
+    }
+
+    int done = 0;  // units before this one
+    bool ok = true;
+    int2 last = make_int2(-1, -1);
+    for (; !w.done(); w.next<DENSE>(p, scan)) {
+        // Q, scaled by 2^qe
+        uint32_t qf[NL][4][2];
+        float qs[2];                           // for heads 2 t4, 2 t4 + 1
+        {
+            const __nv_bfloat16* q = p.Q + (w.t * p.Hkv * p.G + (int64_t)(h0 + h) * p.G + g) * D;
+            uint32_t raw[NL][8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                uint4 a = make_uint4(0, 0, 0, 0), c = a;
+                if (g < p.G) {
+                    a = *reinterpret_cast<const uint4*>(q + 64 * i + 16 * t4);
+                    c = *reinterpret_cast<const uint4*>(q + 64 * i + 16 * t4 + 8);
+                }
+                raw[i][0] = a.x; raw[i][1] = a.y; raw[i][2] = a.z; raw[i][3] = a.w;
+                raw[i][4] = c.x; raw[i][5] = c.y; raw[i][6] = c.z; raw[i][7] = c.w;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = max(top, max(raw[i][j] & 0x7fffu, raw[i][j] >> 16 & 0x7fffu));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the exponent that brings the largest element to [2^14, 2^15)
+            int qe = top == 0 || top >= 0x7f80u ? 0 : 14 + 127 - (int)max(top >> 7, 1u);
+            qe = min(qe, 126);
+            const float up = __uint_as_float((uint32_t)(qe + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const __half2 v = __floats2half2_rn(__uint_as_float(raw[i][j] << 16) * up,
+                                                        __uint_as_float(raw[i][j] & 0xffff0000u) * up);
+                    qf[i][j >> 1][j & 1] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+            const float back = p.scale_log2 * __uint_as_float((uint32_t)(127 - qe) << 23);
+            qs[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
+            qs[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
+        }
+
+        float o[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+        float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+        for (int64_t u = w.a; u < w.b; ++u, ++done) {
+            if (C::NSUB > 1 && done % C::NSUB != sub) continue;
+            const int st = done % C::STAGES;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_to(p.err, smem_u32(&full[st]),
+                                                              (done / C::STAGES) & 1));
+            const uint32_t msk = ok ? mask_s[st] : 0u;
+            if (msk) {
+                const uint32_t at = mine + st * C::STAGE;
+                const float2* sc = sc_s + (st * HG + h) * kKeys + pk;
+                float x[2][4], y[2][4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t kr[2][NL][4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int i = 0; i < NL; ++i)
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(kr[r][i][0]), "=r"(kr[r][i][1]),
+                                           "=r"(kr[r][i][2]), "=r"(kr[r][i][3])
+                                         : "r"(at + koff[i] + (16 * j + 8 * r) * D));
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < NL; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t a[4] = {widen(kr[0][i][q]), widen(kr[1][i][q]),
+                                                   widen(kr[0][i][q] >> 16),
+                                                   widen(kr[1][i][q] >> 16)};
+                            mma_f16(s, a, qf[i][q][0], qf[i][q][1]);
+                        }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float2 f = sc[16 * j + 8 * r];
+                        const bool in = msk >> (16 * j + 8 * r + pk) & 1u;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            x[j][2 * r + c] = in ? s[2 * r + c] * (f.x * qs[c]) : -INFINITY;
+                            y[j][2 * r + c] = x[j][2 * r + c] + f.y;
+                        }
+                    }
+                }
+                float wgt[2][4], fy[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float ax = fmaxf(fmaxf(x[0][c], x[0][c + 2]), fmaxf(x[1][c], x[1][c + 2]));
+                    float ay = fmaxf(fmaxf(y[0][c], y[0][c + 2]), fmaxf(y[1][c], y[1][c + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        ax = fmaxf(ax, __shfl_xor_sync(0xffffffffu, ax, d));
+                        ay = fmaxf(ay, __shfl_xor_sync(0xffffffffu, ay, d));
+                    }
+                    const float nx = fmaxf(mx[c], ax), ny = fmaxf(my[c], ay);
+                    const float ux = nx == -INFINITY ? 0.f : nx, uy = ny == -INFINITY ? 0.f : ny;
+                    const float fx = ex2(mx[c] - ux);
+                    fy[c] = ex2(my[c] - uy);
+                    const float ry = uy - kWeightLog2;
+                    mx[c] = nx;
+                    my[c] = ny;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            sum += ex2(x[j][2 * r + c] - ux);
+                            wgt[j][2 * r + c] = ex2(y[j][2 * r + c] - ry);
+                        }
+                    l[c] = l[c] * fx + sum;
+                }
+                if (__any_sync(0xffffffffu, fy[0] != 1.f || fy[1] != 1.f)) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[i][c] *= fy[c & 1];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t vr[4][VW];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t q = at + voff[e & 1] + (16 * j + (e >> 1) * 8) * D;
+                        if constexpr (VW == 4)
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(vr[e][0]), "=r"(vr[e][1]), "=r"(vr[e][2 % VW]),
+                                           "=r"(vr[e][3 % VW])
+                                         : "r"(q));
+                        else
+                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                                         : "=r"(vr[e][0]), "=r"(vr[e][1])
+                                         : "r"(q));
+                    }
+                    if (msk != 0xffffffffu) {  // what lies in an absent key's place may be NaN
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(msk >> (16 * j + (e >> 1) * 8 + place(2 * t4 + (e & 1))) & 1u))
+#pragma unroll
+                                for (int q = 0; q < VW; ++q) vr[e][q] = 0;
+                    }
+                    uint32_t pf[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const __half2 v = __floats2half2_rn(wgt[j][2 * r], wgt[j][2 * r + 1]);
+                        pf[r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&v));
+                    }
+#pragma unroll
+                    for (int i = 0; i < VW; ++i)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t sel = q ? 0x7362u : 0x5140u;
+                            const uint32_t lo = __byte_perm(vr[0][i], vr[1][i], sel);
+                            const uint32_t hi = __byte_perm(vr[2][i], vr[3][i], sel);
+                            const uint32_t a[4] = {widen(lo), widen(lo >> 16), widen(hi),
+                                                   widen(hi >> 16)};
+                            mma_f16(o[2 * i + q], a, pf[0], pf[1]);
+                        }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
+        }
+
+        // ---- the warps' sums of this row
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+        named_bar_sync(1, kConsumers * 32);  // the row before has been read
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float* q = o_s + (warp * 8 + 2 * t4 + c) * C::OROW + 2 * MT * g;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {  // m tile i, rows g and g + 8: d = 2 MT g + 2 i, + 1
+                q[2 * i] = o[i][c];
+                q[2 * i + 1] = o[i][c + 2];
+            }
+            if (g == 0) m_s[warp * 8 + 2 * t4 + c] = make_float4(mx[c], my[c], l[c], 0.f);
+        }
+        named_bar_sync(1, kConsumers * 32);
+        const bool whole = w.a == 0 && w.b == w.all;
+        if (p.part_row != nullptr && threadIdx.x == 0 && blockIdx.y == 0 && w.a == 0) {
+            // for the merge: the CTAs of this row, named by the one that has its first unit
+            int2 r = make_int2(-1, -1);
+            if (!whole) {
+                const int64_t end = w.all + (DENSE ? scan[w.t] : w.t * w.all);
+                r = make_int2((int)w.t, (int)((end * w.C + w.U - 1) / w.U - 1));
+            }
+            if (p.rows.n <= gridDim.x)
+                p.part_row[w.t] = make_int4(r.x, r.x < 0 ? 0 : (int)blockIdx.x, r.y, 0);
+            else
+                last = r;
+        }
+        bool write = true;
+        if (whole && p.rows.off != nullptr)
+            write = w.t >= p.rows.off[0] && w.t < p.rows.off[p.rows.B];
+        for (int e = threadIdx.x; write && e < HG * p.G * D; e += kConsumers * 32) {
+            const int hq = e / D, d = e % D;
+            const int hl = hq / p.G, hh = hq % p.G;
+            float Mx = -INFINITY, My = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < C::NSUB; ++v) {
+                const float4 m = m_s[(v * HG + hl) * 8 + hh];
+                Mx = fmaxf(Mx, m.x);
+                My = fmaxf(My, m.y);
+            }
+            const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
+            float ls = 0.f, acc = 0.f;
+#pragma unroll
+            for (int v = 0; v < C::NSUB; ++v) {
+                const float4 m = m_s[(v * HG + hl) * 8 + hh];
+                ls += m.z * ex2(m.x - ux);
+                acc += o_s[((v * HG + hl) * 8 + hh) * C::OROW + d] * ex2(m.y - uy);
+            }
+            const int64_t head = (int64_t)h0 * p.G + hq;
+            const int64_t Hq = (int64_t)p.Hkv * p.G;
+            if (whole) {
+                p.O[(w.t * Hq + head) * D + d] =
+                    __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
+                if (p.lse != nullptr && d == 0)
+                    p.lse[w.t * Hq + head] = ls == 0.f ? -INFINITY
+                                                       : (Mx + log2f(ls)) * 0.6931471805599453f;
+            } else {
+                const int64_t at = ((int64_t)blockIdx.x * 2 + (w.a > 0 ? 0 : 1)) * Hq + head;
+                p.part_o[at * D + d] = acc;
+                if (d == 0)
+                    *reinterpret_cast<float4*>(p.part_m + at * 4) = make_float4(Mx, My, ls, 0.f);
+            }
         }
     }
+    if (p.part_row != nullptr && threadIdx.x == 0 && blockIdx.y == 0 && p.rows.n > gridDim.x)
+        p.part_row[blockIdx.x] = make_int4(last.x, (int)blockIdx.x, last.y, 0);
 }
 
-// Merges the slices of one (row, head).
+// Merges one head of a row that several CTAs shared.  part_row has an entry (row,
+// first CTA, last CTA) or -1 per row, or per CTA where rows are more.
 template <int D>
 __global__ void __launch_bounds__(D) combine_kernel(const AttnParams p) {
     pdl_wait();
-    const int64_t Hq = (int64_t)p.Hkv * p.G;
-    const int64_t t = blockIdx.y, head = blockIdx.x;
-    const int d = threadIdx.x;
+    const int4 r = p.part_row[blockIdx.x];
+    if (r.x < 0) return;
+    const int64_t t = r.x;
     if (p.rows.off != nullptr && (t < p.rows.off[0] || t >= p.rows.off[p.rows.B])) return;
-    auto at = [&](int j) { return (t * p.nsplit + j) * Hq + head; };
+    const int64_t Hq = (int64_t)p.Hkv * p.G, head = blockIdx.y;
+    const int d = threadIdx.x;
+    auto at = [&](int j) { return ((int64_t)j * 2 + (j == r.y ? 1 : 0)) * Hq + head; };
     float Mx = -INFINITY, My = -INFINITY;
-    for (int j = 0; j < p.nsplit; ++j) {
-        Mx = fmaxf(Mx, p.part_m[at(j) * 4]);
-        My = fmaxf(My, p.part_m[at(j) * 4 + 1]);
+#pragma unroll 4
+    for (int j = r.y; j <= r.z; ++j) {
+        const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j) * 4);
+        Mx = fmaxf(Mx, m.x);
+        My = fmaxf(My, m.y);
     }
     const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
     float ls = 0.f, acc = 0.f;
-    for (int j = 0; j < p.nsplit; ++j) {
+#pragma unroll 8
+    for (int j = r.y; j <= r.z; ++j) {
         const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j) * 4);
         ls += m.z * ex2(m.x - ux);
         acc += p.part_o[at(j) * D + d] * ex2(m.y - uy);
     }
-    p.O[(t * Hq + head) * D + d] = __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
+    p.O[(t * Hq + head) * D + d] =
+        __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
     if (p.lse != nullptr && d == 0)
         p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
 }
