@@ -312,8 +312,7 @@ __device__ __forceinline__ int64_t row_units(const AttnParams& p, int64_t t) {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -324,6 +323,10 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
     return r;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -486,7 +489,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
     }
     __syncthreads();
 
-    Walk w;
+    Walk w{};
     w.open<DENSE>(p, scan);
 
     if (warp >= kConsumers) {
@@ -587,7 +590,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             }
 #pragma unroll
             for (int h = 0; h < HG; ++h)
-                sc_s[(s * HG + h) * kKeys + lane] = make_float2(ks[h], __log2f(vs[h]));
+                sc_s[(s * HG + h) * kKeys + lane] = make_float2(ks[h], valid ? __log2f(vs[h]) : 0.f);
             if (lane == 0) mask_s[s] = bal;
             __syncwarp();
             if constexpr (DENSE) {
@@ -628,7 +631,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
     const int g = lane >> 2, t4 = lane & 3;
     auto place = [](int m) { return (int)((D == 128 ? 0x37156240u : 0x65742130u) >> (4 * m) & 7u); };
     const int pk = place(g);
-    const uint32_t mine = smem_u32(smem) + h * C::BOX;
+    const uint8_t* mine = smem + h * C::BOX;
     uint32_t koff[NL], voff[2];
 #pragma unroll
     for (int i = 0; i < NL; ++i)
@@ -697,37 +700,38 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                                                               (done / C::STAGES) & 1));
             const uint32_t msk = ok ? mask_s[st] : 0u;
             if (msk) {
-                const uint32_t at = mine + st * C::STAGE;
+                const uint8_t* at = mine + st * C::STAGE;
                 const float2* sc = sc_s + (st * HG + h) * kKeys + pk;
                 float x[2][4], y[2][4];
+                float s[2][4] = {};
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    uint4 kr[2][2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            kr[j][r] = *reinterpret_cast<const uint4*>(at + koff[i] +
+                                                                       (16 * j + 8 * r) * D);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t k0 = word(kr[j][0], q), k1 = word(kr[j][1], q);
+                            const uint32_t a[4] = {widen(k0), widen(k1), widen(k0 >> 16),
+                                                   widen(k1 >> 16)};
+                            mma_f16(s[j], a, qf[i][q][0], qf[i][q][1]);
+                        }
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    uint32_t kr[2][NL][4];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int i = 0; i < NL; ++i)
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(kr[r][i][0]), "=r"(kr[r][i][1]),
-                                           "=r"(kr[r][i][2]), "=r"(kr[r][i][3])
-                                         : "r"(at + koff[i] + (16 * j + 8 * r) * D));
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < NL; ++i)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t a[4] = {widen(kr[0][i][q]), widen(kr[1][i][q]),
-                                                   widen(kr[0][i][q] >> 16),
-                                                   widen(kr[1][i][q] >> 16)};
-                            mma_f16(s, a, qf[i][q][0], qf[i][q][1]);
-                        }
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float2 f = sc[16 * j + 8 * r];
                         const bool in = msk >> (16 * j + 8 * r + pk) & 1u;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            x[j][2 * r + c] = in ? s[2 * r + c] * (f.x * qs[c]) : -INFINITY;
+                            x[j][2 * r + c] = in ? s[j][2 * r + c] * (f.x * qs[c]) : -INFINITY;
                             y[j][2 * r + c] = x[j][2 * r + c] + f.y;
                         }
                     }
@@ -770,16 +774,14 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                     uint32_t vr[4][VW];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t q = at + voff[e & 1] + (16 * j + (e >> 1) * 8) * D;
-                        if constexpr (VW == 4)
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(vr[e][0]), "=r"(vr[e][1]), "=r"(vr[e][2 % VW]),
-                                           "=r"(vr[e][3 % VW])
-                                         : "r"(q));
-                        else
-                            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                                         : "=r"(vr[e][0]), "=r"(vr[e][1])
-                                         : "r"(q));
+                        const uint8_t* q = at + voff[e & 1] + (16 * j + (e >> 1) * 8) * D;
+                        if constexpr (VW == 4) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(q);
+                            vr[e][0] = v.x; vr[e][1] = v.y; vr[e][2 % VW] = v.z; vr[e][3 % VW] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(q);
+                            vr[e][0] = v.x; vr[e][1] = v.y;
+                        }
                     }
                     if (msk != 0xffffffffu) {  // what lies in an absent key's place may be NaN
 #pragma unroll
@@ -884,35 +886,84 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
 
 // Merges one head of a row that several CTAs shared.  part_row has an entry (row,
 // first CTA, last CTA) or -1 per row, or per CTA where rows are more.
+// Latency decides it (a row of 148 parts is 78 KB): all maxima are loaded at
+// once, then D / 4 threads take a part, four loads in flight each.
+constexpr int kCombineThreads = 256;
+constexpr int kMaxParts = 512;
+
 template <int D>
-__global__ void __launch_bounds__(D) combine_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttnParams p) {
+    constexpr int LP = D / 4, NG = kCombineThreads / LP;
+    __shared__ float f_s[kMaxParts];      // 2^(My of a part - My)
+    __shared__ float red_s[3][kCombineThreads / 32];
+    __shared__ float4 o_s[NG][LP];
     pdl_wait();
     const int4 r = p.part_row[blockIdx.x];
     if (r.x < 0) return;
     const int64_t t = r.x;
     if (p.rows.off != nullptr && (t < p.rows.off[0] || t >= p.rows.off[p.rows.B])) return;
     const int64_t Hq = (int64_t)p.Hkv * p.G, head = blockIdx.y;
-    const int d = threadIdx.x;
-    auto at = [&](int j) { return ((int64_t)j * 2 + (j == r.y ? 1 : 0)) * Hq + head; };
+    const int n = r.z - r.y + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto at = [&](int j) { return ((int64_t)(r.y + j) * 2 + (j == 0 ? 1 : 0)) * Hq + head; };
+    float4 m[kMaxParts / kCombineThreads];
     float Mx = -INFINITY, My = -INFINITY;
-#pragma unroll 4
-    for (int j = r.y; j <= r.z; ++j) {
-        const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j) * 4);
-        Mx = fmaxf(Mx, m.x);
-        My = fmaxf(My, m.y);
+#pragma unroll
+    for (int q = 0; q < kMaxParts / kCombineThreads; ++q) {
+        const int j = q * kCombineThreads + threadIdx.x;
+        m[q] = j < n ? *reinterpret_cast<const float4*>(p.part_m + at(j) * 4)
+                     : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        Mx = fmaxf(Mx, m[q].x);
+        My = fmaxf(My, m[q].y);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, d));
+        My = fmaxf(My, __shfl_xor_sync(0xffffffffu, My, d));
+    }
+    if (lane == 0) {
+        red_s[0][warp] = Mx;
+        red_s[1][warp] = My;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kCombineThreads / 32; ++q) {
+        Mx = fmaxf(Mx, red_s[0][q]);
+        My = fmaxf(My, red_s[1][q]);
     }
     const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
-    float ls = 0.f, acc = 0.f;
-#pragma unroll 8
-    for (int j = r.y; j <= r.z; ++j) {
-        const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j) * 4);
-        ls += m.z * ex2(m.x - ux);
-        acc += p.part_o[at(j) * D + d] * ex2(m.y - uy);
+    float ls = 0.f;
+#pragma unroll
+    for (int q = 0; q < kMaxParts / kCombineThreads; ++q) {
+        const int j = q * kCombineThreads + threadIdx.x;
+        ls += m[q].z * ex2(m[q].x - ux);
+        if (j < n) f_s[j] = ex2(m[q].y - uy);
     }
-    p.O[(t * Hq + head) * D + d] =
-        __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
-    if (p.lse != nullptr && d == 0)
-        p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    if (lane == 0) red_s[2][warp] = ls;
+    __syncthreads();
+    ls = 0.f;
+#pragma unroll
+    for (int q = 0; q < kCombineThreads / 32; ++q) ls += red_s[2][q];
+    const int g = threadIdx.x / LP, c = threadIdx.x % LP;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = g; j < n; j += NG) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at(j) * D + 4 * c);
+        const float f = f_s[j];
+        acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+    }
+    o_s[g][c] = acc;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float a = 0.f;
+        const int groups = n < NG ? n : NG;
+        for (int q = 0; q < groups; ++q) a += reinterpret_cast<const float*>(o_s[q])[threadIdx.x];
+        p.O[(t * Hq + head) * D + threadIdx.x] =
+            __float2bfloat16_rn(ls == 0.f ? 0.f : a / ls * kWeightScale * ex2(My - Mx));
+        if (p.lse != nullptr && threadIdx.x == 0)
+            p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
+    }
 }
 
 }  // namespace kv8
