@@ -572,47 +572,25 @@ def decode_combine_shards(part_o, part_ml, O=None, stream=None, err=None):
 
 # ------------------------------------------------------------------ rotary positions
 
-TYPE_CODES = {torch.bfloat16: 0, torch.float32: 1, torch.float8_e4m3fn: 2}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
-
-def _alloc(shape, dtype, device, stream) -> torch.Tensor:
-    """A device tensor that belongs to the launch stream, so that its memory
-    is not handed out again before the stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
-                  else torch.cuda.default_stream())
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+_native_module = None
 
 
-def _alloc_like(t: torch.Tensor, dtype, stream) -> torch.Tensor:
-    if stream is None:
-        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
-    return _alloc(t.shape, dtype, t.device, stream)
-
-
-def _heads(t: torch.Tensor, name: str, L: int, d: int, dtype: torch.dtype):
-    """Pointer, token stride and number of heads of an array [L][heads][d]
-    whose heads are dense (a part of a wider row is fine)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != _current_device():
-        raise ValueError(f"{name} is on {t.device}, but the library launches on the current "
-                         f"device cuda:{torch.cuda.current_device()}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [{L}][heads][{d}], got {tuple(t.shape)}")
-    n, H, e = t.shape
-    if n != L or e != d:
-        raise ValueError(f"{name} must be [{L}][heads][{d}], got {tuple(t.shape)}")
-    sn, sh, se = t.stride()
-    if (se != 1 and d > 1) or (sh != d and H > 1):
-        raise ValueError(f"{name}: each token's heads must be dense, got strides {t.stride()}")
-    return t.data_ptr(), (sn if L > 1 else H * d), H
+def _load_native():
+    """The module that checks and marshals the arguments of the calls below
+    (csrc/binding.cpp; raises if it has not been built)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        try:
+            from . import _native as m
+        except ImportError as e:
+            raise RuntimeError("the package's _native.so is missing or does not load; build it "
+                               "with `python -m sparse_long_context_02_b200.build`") from e
+        m.bind(LIB_PATH, _check)
+        _native_module = m
+    return _native_module
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -631,44 +609,6 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
     return freqs.to(device if device is not None else "cuda"), m.value
 
 
-def _rope(name, q, k, positions, freqs, rot_scale, out_scale, offset, interleaved, out_dtype,
-          q_out, k_out, stream, err):
-    L, Hq, d = q.shape
-    if q.dtype not in TYPE_CODES:
-        raise ValueError(f"{name}: unsupported dtype {q.dtype}")
-    if out_dtype is None:
-        out_dtype = q_out.dtype if q_out is not None else q.dtype
-    if out_dtype not in TYPE_CODES:
-        raise ValueError(f"{name}: unsupported out_dtype {out_dtype}")
-    if positions.dtype != torch.int64 or positions.numel() != L:
-        raise ValueError(f"{name}: positions must be {L} int64")
-    if freqs.dtype != torch.int64:
-        raise ValueError(f"{name}: freqs must be int64 (rope_freqs)")
-    qp, qs, _ = _heads(q, "q", L, d, q.dtype)
-    if q_out is None:
-        q_out = _alloc_like(q, out_dtype, stream)
-    qop, qos, Hqo = _heads(q_out, "q_out", L, d, out_dtype)
-    kp = kop = None
-    ks = kos = Hk = 0
-    if k is not None:
-        kp, ks, Hk = _heads(k, "k", L, d, q.dtype)
-        if k_out is None:
-            k_out = _alloc_like(k, out_dtype, stream)
-        kop, kos, Hko = _heads(k_out, "k_out", L, d, out_dtype)
-        if Hko != Hk:
-            raise ValueError(f"{name}: k_out has {Hko} heads, k {Hk}")
-    elif k_out is not None:
-        raise ValueError(f"{name}: k_out without k")
-    if Hqo != Hq:
-        raise ValueError(f"{name}: q_out has {Hqo} heads, q {Hq}")
-    scales = (rot_scale, out_scale) if out_scale is not None else (rot_scale,)
-    _check(getattr(lib(), name)(
-        qp, kp, _dev(positions, "positions", 8), _dev(freqs, "freqs", 8), L, Hq, Hk, d, offset,
-        2 * freqs.numel(), 1 if interleaved else 0, *scales, TYPE_CODES[q.dtype],
-        TYPE_CODES[out_dtype], qs, ks, qos, kos, qop, kop, _err(err), _stream(stream)), name)
-    return q_out, k_out
-
-
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
          freqs: torch.Tensor, rot_scale: float = 1.0, out_scale: float = 1.0, offset: int = 0,
          interleaved: bool = False, out_dtype: Optional[torch.dtype] = None,
@@ -680,8 +620,9 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
     is [offset, offset + 2 len(freqs)) of each head.  out_dtype bfloat16,
     float32 or float8_e4m3fn (the indexer's q_I and k_I, times out_scale).
     q_out / k_out may be q and k themselves.  Returns (q_out, k_out)."""
-    return _rope("dsa_rope", q, k, positions, freqs, rot_scale, out_scale, offset, interleaved,
-                 out_dtype, q_out, k_out, stream, err)
+    return (_native_module or _load_native()).rope(
+        False, q, k, positions, freqs, rot_scale, out_scale, offset, interleaved, out_dtype, q_out,
+        k_out, stream, err)
 
 
 def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
@@ -691,43 +632,12 @@ def rope_backward(dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch
                   stream=None, err=None):
     """Gradients with respect to rope's q and k (out_scale 1) from those with
     respect to its outputs (such as sparse_attn_backward's dQ and dK)."""
-    return _rope("dsa_rope_backward", dq, dk, positions, freqs, rot_scale, None, offset,
-                 interleaved, out_dtype, q_out, k_out, stream, err)
+    return (_native_module or _load_native()).rope(
+        True, dq, dk, positions, freqs, rot_scale, 1.0, offset, interleaved, out_dtype, q_out,
+        k_out, stream, err)
 
 
 # ------------------------------------------------------------------ 8-bit cache
-
-def _pools(k8, v8, k_scale, v_scale, block_table, seq_lens):
-    """Checks a cache's pools and tables; returns the pointers and sizes."""
-    if k8.dim() != 4 or v8.shape != k8.shape:
-        raise ValueError("k8 and v8 must be [pages][page][Hkv][d] of one shape, got "
-                         f"{tuple(k8.shape)} and {tuple(v8.shape)}")
-    P, page, Hkv, d = k8.shape
-    for t, name in ((k8, "k8"), (v8, "v8")):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise ValueError(f"{name} must be float8_e4m3fn or uint8, got {t.dtype}")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype != torch.float32 or t.shape != (P, Hkv):
-            raise ValueError(f"{name} must be [{P}][{Hkv}] float32")
-    for t, name, dims in ((block_table, "block_table", 2), (seq_lens, "seq_lens", 1)):
-        if t.dtype != torch.int32 or t.dim() != dims:
-            raise ValueError(f"{name} must be int32 with {dims} dimension(s)")
-    B, M = block_table.shape
-    if seq_lens.shape[0] != B:
-        raise ValueError(f"seq_lens must have {B} entries, one per block_table row")
-    return ((_dev(k8, "k8", 1), _dev(v8, "v8", 1), _dev(k_scale, "k_scale", 4),
-             _dev(v_scale, "v_scale", 4)),
-            (_dev(block_table, "block_table", 4), M, _dev(seq_lens, "seq_lens", 4)),
-            P, page, Hkv, d, B)
-
-
-def _offsets(t: Optional[torch.Tensor], name: str, B: int) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.numel() != B + 1:
-        raise ValueError(f"{name} must be {B + 1} int32")
-    return _dev(t, name, 4)
-
 
 def kv8_append(K: torch.Tensor, V: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor,
                k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
@@ -738,53 +648,14 @@ def kv8_append(K: torch.Tensor, V: torch.Tensor, k8: torch.Tensor, v8: torch.Ten
     sequence: rows [new_off[b], new_off[b + 1]), or row b without new_off.
     k8, v8 [pages][page][Hkv][d] e4m3 and k_scale, v_scale [pages][Hkv] are
     updated in place; seq_lens is not (the caller adds the new tokens)."""
-    pools, seqs, P, page, Hkv, d, B = _pools(k8, v8, k_scale, v_scale, block_table, seq_lens)
-    T = K.shape[0]
-    kp, ks, Hk = _heads(K, "K", T, d, torch.bfloat16)
-    vp, vs, Hv = _heads(V, "V", T, d, torch.bfloat16)
-    if Hk != Hkv or Hv != Hkv:
-        raise ValueError(f"K and V must have {Hkv} heads")
-    _check(lib().dsa_kv8_append(kp, vp, T, ks, vs, *pools, P, page, *seqs,
-                                _offsets(new_off, "new_off", B), B, Hkv, d, _err(err),
-                                _stream(stream)), "dsa_kv8_append")
+    (_native_module or _load_native()).kv8_append(K, V, k8, v8, k_scale, v_scale, block_table,
+                                             seq_lens, new_off, stream, err)
 
 
 def attn_kv8_workspace_size(T: int, keys: int, Hq: int, Hkv: int, d: int) -> int:
     """Bytes of workspace for T rows over at most `keys` keys each: k for
     sparse_attn_kv8, block_table columns x page for attn_kv8."""
     return lib().dsa_attn_kv8_workspace_size(T, keys, Hq, Hkv, d)
-
-
-def _attn_kv8(name, Q, k8, v8, k_scale, v_scale, block_table, seq_lens, idx, scale, row_off, O,
-              lse, workspace, stream, err):
-    pools, (tp, M, lp), P, page, Hkv, d, B = _pools(k8, v8, k_scale, v_scale, block_table,
-                                                    seq_lens)
-    if Q.dim() != 3 or Q.shape[2] != d or Q.dtype != torch.bfloat16:
-        raise ValueError(f"Q must be [T][Hq][{d}] bfloat16, got {tuple(Q.shape)} {Q.dtype}")
-    T, Hq, _ = Q.shape
-    if O is None:
-        O = _alloc_like(Q, torch.bfloat16, stream)
-    elif O.shape != Q.shape or O.dtype != torch.bfloat16:
-        raise ValueError("O must have Q's shape, in bfloat16")
-    if lse is not None and (lse.shape != (T, Hq) or lse.dtype != torch.float32):
-        raise ValueError(f"lse must be [{T}][{Hq}] float32")
-    if idx is not None:
-        if idx.dim() != 2 or idx.shape[0] != T or idx.dtype != torch.int32:
-            raise ValueError(f"idx must be [{T}][k] int32")
-        keys = idx.shape[1]
-        sel = (_dev(idx, "idx", 4), keys)
-    else:
-        keys, sel = M * page, ()
-    need = attn_kv8_workspace_size(T, keys, Hq, Hkv, d)
-    if workspace is None and need:
-        workspace = _alloc(need, torch.uint8, Q.device, stream)
-    ws = (None, 0) if workspace is None else (
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
-    _check(getattr(lib(), name)(
-        _dev(Q, "Q", 2), *pools, P, page, tp, M, lp, _offsets(row_off, "row_off", B), B, T, *sel,
-        Hq, Hkv, d, float(scale), _dev(O, "O", 2), _dev(lse, "lse", 4) if lse is not None else None,
-        *ws, _err(err), _stream(stream)), name)
-    return O
 
 
 def sparse_attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
@@ -797,8 +668,11 @@ def sparse_attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale
     attends to positions idx[t] (-1: none) of its sequence, row b of sequence
     b, or rows [row_off[b], row_off[b + 1]).  Returns O [T][Hq][d]; `lse` as
     sparse_attn_prefill.  Calls that may overlap need a workspace each."""
-    return _attn_kv8("dsa_sparse_attn_kv8", Q, k8, v8, k_scale, v_scale, block_table, seq_lens,
-                     idx, scale, row_off, O, lse, workspace, stream, err)
+    if idx is None:
+        raise ValueError("idx must be [T][k] int32")
+    return (_native_module or _load_native()).attn_kv8(Q, k8, v8, k_scale, v_scale, block_table,
+                                                  seq_lens, idx, scale, row_off, O, lse,
+                                                  workspace, stream, err)
 
 
 def attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
@@ -808,5 +682,6 @@ def attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch
              workspace: Optional[torch.Tensor] = None, stream=None, err=None) -> torch.Tensor:
     """sparse_attn_kv8 over every key of the sequence; with row_off, where the
     rows are a sequence's last tokens, causally."""
-    return _attn_kv8("dsa_attn_kv8", Q, k8, v8, k_scale, v_scale, block_table, seq_lens, None,
-                     scale, row_off, O, lse, workspace, stream, err)
+    return (_native_module or _load_native()).attn_kv8(Q, k8, v8, k_scale, v_scale, block_table,
+                                                  seq_lens, None, scale, row_off, O, lse,
+                                                  workspace, stream, err)

@@ -3,6 +3,7 @@ in place, for sm_100a."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -13,6 +14,9 @@ SOURCES = [os.path.join(CSRC, "dsa_lib.cu")]
 # not part of the ABI
 PROBE_SOURCE = os.path.join(CSRC, "probe_l2.cu")
 PROBE_PATH = os.path.join(HERE, "libdsa_probe.so")
+# the Python side's argument marshalling (host code, torch's C++ API)
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_native.so")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "dsa.h")]
 
@@ -40,8 +44,32 @@ def build_probe(force: bool = False) -> str:
     return PROBE_PATH
 
 
+def build_binding(force: bool = False) -> str:
+    deps = (BINDING_SOURCE, os.path.join(ROOT, "include", "dsa.h"))
+    if (not force and os.path.exists(BINDING_PATH)
+            and os.path.getmtime(BINDING_PATH) >= max(os.path.getmtime(d) for d in deps)):
+        return BINDING_PATH
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    lib = os.path.join(at, "lib")
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+        "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(at, "include"),
+        "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+        "-isystem", os.path.join(cuda, "include"),
+        "-isystem", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SOURCE,
+        "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+        "-ldl"])
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     build_probe(force)
+    build_binding(force)
     if (not force and os.path.exists(LIB_PATH)
             and os.path.getmtime(LIB_PATH) >= max(os.path.getmtime(d) for d in DEPS)):
         return LIB_PATH

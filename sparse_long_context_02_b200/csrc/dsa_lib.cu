@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1625,7 +1626,13 @@ dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int 
             if (!make_pool_map(&maps[w], p.code[w], D, p.Hkv, p.pages * page, rows))
                 return fail(DSA_ERR_CUDA, "%s: tensor map", fn);
     }
-    CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    static std::atomic<uint64_t> ready{0};  // devices that know the kernel's shared memory
+    int dev = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    if (dev > 63 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+        if (dev <= 63) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
     kern<<<dim3((unsigned)ctas, (unsigned)(p.Hkv / HG)), kv::kAttnThreads, C::SMEM, st>>>(
         p, maps[0], maps[1]);
     CUDA_TRY(cudaGetLastError());
