@@ -1556,8 +1556,10 @@ bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page =
 template <int PAGE, int D>
 dsa_status_t launch_append(const char* fn, const dsa::kv8::AppendParams& p, int64_t units,
                            cudaStream_t st) {
+    constexpr int TEAMS = dsa::kv8::AppendCfg<PAGE, D>::TEAMS;
     dsa::kv8::append_kernel<PAGE, D>
-        <<<dim3((unsigned)(units * p.Hkv), 2), dsa::kv8::AppendCfg<PAGE, D>::THREADS, 0, st>>>(p);
+        <<<(unsigned)((units * 2 * p.Hkv + TEAMS - 1) / TEAMS), dsa::kv8::kAppendThreads, 0, st>>>(
+            p, (int)units);
     CUDA_TRY(cudaGetLastError());
     return ok();
 }
@@ -1565,6 +1567,14 @@ dsa_status_t launch_append(const char* fn, const dsa::kv8::AppendParams& p, int6
 template <int D>
 dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendParams& p,
                              int64_t units, cudaStream_t st) {
+    if (p.rows.off == nullptr) {
+        const int log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+        const int64_t warps = (int64_t)p.rows.B * 2 * p.Hkv, per = dsa::kv8::kAppendThreads / 32;
+        dsa::kv8::append_one_kernel<D>
+            <<<(unsigned)((warps + per - 1) / per), dsa::kv8::kAppendThreads, 0, st>>>(p, log2);
+        CUDA_TRY(cudaGetLastError());
+        return ok();
+    }
     if (page == 16) return launch_append<16, D>(fn, p, units, st);
     if (page == 32) return launch_append<32, D>(fn, p, units, st);
     if (page == 64) return launch_append<64, D>(fn, p, units, st);
@@ -1774,7 +1784,7 @@ dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int64_t k_s
                     "%s: k_stride = %lld, v_stride = %lld (multiples of 8, at least Hkv x d)", fn,
                     (long long)k_stride, (long long)v_stride);
     const int64_t units = new_off == nullptr ? B : T / page + 2 * (int64_t)B;
-    if (units * Hkv >= (int64_t(1) << 31)) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
+    if (units * 2 * Hkv >= (int64_t(1) << 31)) return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows", fn);
     dsa::kv8::AppendParams p{};
     p.x[0] = static_cast<const __nv_bfloat16*>(K);
     p.x[1] = static_cast<const __nv_bfloat16*>(V);

@@ -16,6 +16,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace dsa {
@@ -65,23 +67,16 @@ __device__ __forceinline__ float value_of(uint32_t code) {
     return __half2float(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3));
 }
 
-// Units of work: (sequence, touched page).  A sequence's n new tokens touch at
-// most n / page + 2 pages, and off[b + 1] / page - off[b] / page >= n / page, so the
-// unit ranges starting at off[b] / page + 2 b never overlap, and T / page + 2 B
-// units cover all without knowing the lengths on the host.  Returns false for
-// a unit that has nothing to do.
+// Units of work of a call with offsets: (sequence, touched page).  A sequence's n
+// new tokens touch at most n / page + 2 pages, and off[b + 1] / page - off[b] / page >=
+// n / page, so the unit ranges starting at off[b] / page + 2 b never overlap, and
+// T / page + 2 B units cover all without knowing the lengths on the host.
+// Returns false for a unit that has nothing to do.
 template <int PAGE>
-__device__ __forceinline__ bool find_unit(const AppendParams& p, int u, int& b, int64_t& r0,
-                                          int64_t& n, int& col) {
+__device__ __forceinline__ bool find_unit(const AppendParams& p, int u, bool report, int& b,
+                                          int64_t& r0, int64_t& n, int& len, int& col) {
     const Rows& rw = p.rows;
-    if (rw.off == nullptr) {
-        b = u;
-        r0 = u;
-        n = 1;
-        col = p.lens[b] >= 0 ? p.lens[b] / PAGE : 0;
-        return p.lens[b] >= 0;
-    }
-    auto base = [&](int i) { return max(rw.off[i], 0) / PAGE + 2 * i; };
+    auto base = [&](int i) { return max(__ldg(rw.off + i), 0) / PAGE + 2 * i; };
     int lo = 0, hi = rw.B - 1;  // the last b with base(b) <= u
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -89,122 +84,234 @@ __device__ __forceinline__ bool find_unit(const AppendParams& p, int u, int& b, 
         else hi = mid - 1;
     }
     b = lo;
-    r0 = rw.off[b];
-    const int64_t r1 = rw.off[b + 1];
+    len = __ldg(p.lens + b);
+    r0 = __ldg(rw.off + b);
+    const int64_t r1 = __ldg(rw.off + b + 1);
     if (r0 < 0 || r1 < r0 || r1 > rw.n) {
-        if (threadIdx.x == 0) record_error_to(p.err, 2);
+        if (report) record_error_to(p.err, 2);
         return false;
     }
     n = r1 - r0;
-    const int len = p.lens[b];
-    if (len < 0 || n == 0) return false;
-    const int64_t c = len / PAGE + (u - base(b));
-    if (u < base(b) || c > (len + n - 1) / PAGE) return false;
+    const int first = max((int)r0, 0) / PAGE + 2 * b;
+    if (len < 0 || n == 0 || u < first) return false;
+    const int64_t c = len / PAGE + (u - first);
+    if (c > (len + n - 1) / PAGE) return false;
     if (c >= p.M) {
-        if (threadIdx.x == 0) record_error_to(p.err, 2);
+        if (report) record_error_to(p.err, 2);
         return false;
     }
     col = (int)c;
     return true;
 }
 
+// The page's scale under new elements whose largest has the bf16 bits `top`.
+__device__ __forceinline__ float scale_for(uint32_t top) {
+    return __uint_as_float((uint32_t)(scale_exp(__uint_as_float(top << 16)) + 127) << 23);
+}
+
+// 1 / s where that is exact (powers of two, all that this file stores), else 0.
+__device__ __forceinline__ float exact_inverse(float s) {
+    const uint32_t u = __float_as_uint(s), e = u >> 23;
+    return (u & 0x7fffffu) == 0 && e >= 1 && e <= 253 ? __uint_as_float((254 - e) << 23) : 0.f;
+}
+
+// Codes of two finite bf16 elements under a scale with an exact inverse ...
+__device__ __forceinline__ uint32_t codes_of(uint32_t two, float inv) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(r)
+        : "f"(__uint_as_float(two & 0xffff0000u) * inv), "f"(__uint_as_float(two << 16) * inv));
+    return r;
+}
+
+// ... and of any two under any scale.
+__device__ __forceinline__ uint32_t any_codes_of(uint32_t two, float s) {
+    return code_of(__fdiv_rn(__uint_as_float(two << 16), s)) |
+           code_of(__fdiv_rn(__uint_as_float(two & 0xffff0000u), s)) << 8;
+}
+
+// Rounds `count` 8-code pieces again under a scale that grew by 1 / f; piece e lies
+// at row e / PER_ROW of the page.
+template <int PER_ROW>
+__device__ __forceinline__ void round_again(uint8_t* page, int64_t row, int count, float f, int at,
+                                            int step) {
+    for (int e = at; e < count; e += step) {
+        uint2* q = reinterpret_cast<uint2*>(page + e / PER_ROW * row + e % PER_ROW * 8);
+        const uint2 old = *q;
+        uint32_t o[2] = {old.x, old.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t r = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                r |= code_of(value_of(o[j] >> (8 * k) & 0xffu) * f) << (8 * k);
+            o[j] = r;
+        }
+        *q = make_uint2(o[0], o[1]);
+    }
+}
+
+constexpr int kAppendThreads = 256;
+
 template <int PAGE, int D>
 struct AppendCfg {
-    static constexpr int VECS = PAGE * D / 8;  // 8-element pieces of a (page, head)
-    static constexpr int THREADS = VECS < 256 ? 128 : 256;
-    static constexpr int VPT = VECS / THREADS;
+    static constexpr int VECS = PAGE * D / 8;          // 8-element pieces of a (page, head)
+    static constexpr int TEAM = VECS / 128 < 8 ? VECS / 128 : 8;  // warps that share one
+    static constexpr int TEAMS = kAppendThreads / 32 / TEAM;
+    static constexpr int VPT = VECS / (32 * TEAM);     // 4, or 8 for the largest page
     static constexpr int PER_ROW = D / 8;
+    static constexpr int ROWS = 32 * TEAM / PER_ROW;   // rows that a team takes at once
 };
 
-// One CTA per (unit, head, K or V): the page's new elements stay in registers
-// between the maximum and the rounding, so they are read once.
+// Pieces of prompts: a team of warps per (unit, K or V, head), neighbouring
+// heads side by side.  The page's new elements stay in registers between the
+// maximum and the rounding, so they are read once; their loads go out before the
+// page is looked up, four (eight) of 16 bytes per thread.
 template <int PAGE, int D>
-__global__ void __launch_bounds__(AppendCfg<PAGE, D>::THREADS) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, AppendCfg<PAGE, D>::VPT == 4 ? 6 : 4)
+append_kernel(const AppendParams p, int units) {
     using C = AppendCfg<PAGE, D>;
-    const int h = blockIdx.x % p.Hkv, w = blockIdx.y;
-    int b, col;
-    int64_t r0, n;
-    if (!find_unit<PAGE>(p, blockIdx.x / p.Hkv, b, r0, n, col)) return;
-    const int32_t pg = col < p.M ? p.table[(int64_t)b * p.M + col] : -1;
-    if (pg < 0 || pg >= p.pages) {
-        if (threadIdx.x == 0) record_error_to(p.err, 2);
-        return;
-    }
-    const int len = p.lens[b];
+    __shared__ uint32_t top_s[kAppendThreads / 32];
+    const int warp = threadIdx.x >> 5, team = warp / C::TEAM;
+    const int me = threadIdx.x - team * C::TEAM * 32;  // thread of the team
+    const uint32_t item = blockIdx.x * C::TEAMS + team, hkv = p.Hkv;  // below 2^31 + 8
+    const uint32_t u = item / (2 * hkv), uh = item - u * 2 * hkv;
+    const int w = uh >= hkv, h = uh - (w ? hkv : 0);
+    int b = 0, len = 0, col = 0;
+    int64_t r0 = 0, n = 0;
+    bool live = u < (uint32_t)units && find_unit<PAGE>(p, (int)u, me == 0, b, r0, n, len, col);
     // slot i of the page is the sequence's position col * PAGE + i
     const int64_t at = (int64_t)col * PAGE;
     const int first = len > at ? (int)(len - at) : 0;
-    const int last = len + n < at + PAGE ? (int)(len + n - at) : PAGE;
+    const int last = !live ? 0 : len + n < at + PAGE ? (int)(len + n - at) : PAGE;
 
+    const int slot = me / C::PER_ROW, c = me % C::PER_ROW * 8;  // + ROWS i: this thread's pieces
     uint4 v[C::VPT];
-    float amax = 0.f;
+    {
+        const __nv_bfloat16* x = (w ? p.x[1] : p.x[0]) + (r0 + at + slot - len) * (w ? p.xs[1] : p.xs[0]) + h * D + c;
+        const int64_t step = C::ROWS * (w ? p.xs[1] : p.xs[0]);
 #pragma unroll
-    for (int i = 0; i < C::VPT; ++i) {
-        const int e = i * C::THREADS + threadIdx.x;
-        const int slot = e / C::PER_ROW, c = e % C::PER_ROW * 8;
-        if (slot >= first && slot < last)
-            v[i] = *reinterpret_cast<const uint4*>(p.x[w] + (r0 + at + slot - len) * p.xs[w] +
-                                                   (int64_t)h * D + c);
-        else
+        for (int i = 0; i < C::VPT; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < C::VPT; ++i) {
-        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float lo = __uint_as_float((q[j] & 0x7fffu) << 16);
-            const float hi = __uint_as_float(q[j] & 0x7fff0000u);
-            if (lo < INFINITY) amax = fmaxf(amax, lo);
-            if (hi < INFINITY) amax = fmaxf(amax, hi);
+            if (slot + C::ROWS * i >= first && slot + C::ROWS * i < last)
+                v[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * step));
         }
     }
-    __shared__ uint32_t top_s;
-    if (threadIdx.x == 0) top_s = 0;
-    __syncthreads();
-    // non-negative floats order as their bits
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-    if ((threadIdx.x & 31) == 0) atomicMax(&top_s, m);
-    float* sp = p.scale[w] + (int64_t)pg * p.Hkv + h;
+    const int32_t pg = live ? __ldg(p.table + (int64_t)b * p.M + col) : 0;
+    if (pg < 0 || pg >= p.pages) {
+        if (me == 0) record_error_to(p.err, 2);
+        live = false;
+    }
+    float* sp = (w ? p.scale[1] : p.scale[0]) + (int64_t)(live ? pg : 0) * p.Hkv + h;
     const float was = *sp;
-    __syncthreads();
-    const float need = __uint_as_float((uint32_t)(scale_exp(__uint_as_float(top_s)) + 127) << 23);
-    const float now = first > 0 ? fmaxf(was, need) : need;
-    if (threadIdx.x == 0) *sp = now;
-    uint8_t* page = p.code[w] + ((int64_t)pg * PAGE * p.Hkv + h) * D;
-    const int64_t row = (int64_t)p.Hkv * D;
-    if (first > 0 && now != was) {  // the older codes under the larger scale
-        const float f = __fdiv_rn(was, now);
-        for (int e = threadIdx.x; e < first * C::PER_ROW; e += C::THREADS) {
-            uint2* q = reinterpret_cast<uint2*>(page + e / C::PER_ROW * row + e % C::PER_ROW * 8);
-            const uint2 old = *q;
-            uint32_t o[2] = {old.x, old.y};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t r = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    r |= code_of(value_of(o[j] >> (8 * k) & 0xffu) * f) << (8 * k);
-                o[j] = r;
-            }
-            *q = make_uint2(o[0], o[1]);
-        }
-    }
+    uint32_t two = 0;  // bf16 magnitudes order as their bits
 #pragma unroll
     for (int i = 0; i < C::VPT; ++i) {
-        const int e = i * C::THREADS + threadIdx.x;
-        const int slot = e / C::PER_ROW, c = e % C::PER_ROW * 8;
-        if (slot < first || slot >= last) continue;
-        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            o[j] = code_of(__fdiv_rn(__uint_as_float(q[2 * j] << 16), now)) |
-                   code_of(__fdiv_rn(__uint_as_float(q[2 * j] & 0xffff0000u), now)) << 8 |
-                   code_of(__fdiv_rn(__uint_as_float(q[2 * j + 1] << 16), now)) << 16 |
-                   code_of(__fdiv_rn(__uint_as_float(q[2 * j + 1] & 0xffff0000u), now)) << 24;
-        *reinterpret_cast<uint2*>(page + slot * row + c) = make_uint2(o[0], o[1]);
+        two = __vmaxu2(two, __vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu));
+        two = __vmaxu2(two, __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
     }
+    auto team_max = [&](uint32_t m) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (C::TEAM > 1) {
+            if ((threadIdx.x & 31) == 0) top_s[warp] = m;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < C::TEAM; ++i) m = max(m, top_s[team * C::TEAM + i]);
+        }
+        return m;
+    };
+    uint32_t top = team_max(max(two & 0xffffu, two >> 16));
+    const bool odd = top >= 0x7f80u;
+    const bool again = C::TEAM > 1 ? __syncthreads_or(odd) : odd;
+    if (again) {  // infinities or NaN among them: the largest of the others
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < C::VPT; ++i) {
+            const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t lo = q[j] & 0x7fffu, hi = q[j] >> 16 & 0x7fffu;
+                if (lo < 0x7f80u) m = max(m, lo);
+                if (hi < 0x7f80u) m = max(m, hi);
+            }
+        }
+        top = team_max(m);
+    }
+    if (!live) return;
+    const float need = scale_for(top);
+    const float now = first > 0 ? fmaxf(was, need) : need;
+    if (me == 0) *sp = now;
+    uint8_t* page = (w ? p.code[1] : p.code[0]) + ((int64_t)pg * PAGE * p.Hkv + h) * D;
+    const int64_t row = (int64_t)p.Hkv * D;
+    if (first > 0 && now != was)  // the older codes under the larger scale
+        round_again<C::PER_ROW>(page, row, first * C::PER_ROW, __fdiv_rn(was, now), me,
+                                32 * C::TEAM);
+    const float inv = exact_inverse(now);
+    auto store = [&](auto exact) {
+#pragma unroll
+        for (int i = 0; i < C::VPT; ++i) {
+            if (slot + C::ROWS * i < first || slot + C::ROWS * i >= last) continue;
+            auto codes = [&](uint32_t q) {
+                return decltype(exact)::value ? codes_of(q, inv) : any_codes_of(q, now);
+            };
+            *reinterpret_cast<uint2*>(page + (slot + C::ROWS * i) * row + c) =
+                make_uint2(codes(v[i].x) | codes(v[i].y) << 16,
+                           codes(v[i].z) | codes(v[i].w) << 16);
+        }
+    };
+    if (inv != 0.f && !odd) store(std::true_type{});
+    else store(std::false_type{});
+}
+
+// One new token for each sequence: a warp per (sequence, K or V, head).
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) append_one_kernel(const AppendParams p,
+                                                                    int page_log2) {
+    constexpr int W = D / 64;  // 32-bit words of a lane
+    const int lane = threadIdx.x & 31;
+    const uint32_t item = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5), hkv = p.Hkv;
+    const int64_t b = item / (2 * hkv);
+    const uint32_t uh = item - (uint32_t)b * 2 * hkv;
+    const int w = uh >= hkv, h = uh - (w ? hkv : 0);
+    if (b >= p.rows.B) return;
+    const int len = __ldg(p.lens + b);
+    uint32_t v[W];
+    const uint32_t* x = reinterpret_cast<const uint32_t*>((w ? p.x[1] : p.x[0]) + b * (w ? p.xs[1] : p.xs[0]) + (int64_t)h * D) + W * lane;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = __ldg(x + i);
+    if (len < 0) return;
+    const int col = len >> page_log2, first = len & ((1 << page_log2) - 1);
+    const int32_t pg = col < p.M ? __ldg(p.table + b * p.M + col) : -1;
+    if (pg < 0 || pg >= p.pages) {
+        if (lane == 0) record_error_to(p.err, 2);
+        return;
+    }
+    float* sp = (w ? p.scale[1] : p.scale[0]) + (int64_t)pg * p.Hkv + h;
+    const float was = *sp;
+    uint32_t raw = 0, top = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const uint32_t lo = v[i] & 0x7fffu, hi = v[i] >> 16 & 0x7fffu;
+        raw = max(raw, max(lo, hi));
+        if (lo < 0x7f80u) top = max(top, lo);
+        if (hi < 0x7f80u) top = max(top, hi);
+    }
+    raw = __reduce_max_sync(0xffffffffu, raw);
+    const float need = scale_for(__reduce_max_sync(0xffffffffu, top));
+    const float now = first > 0 ? fmaxf(was, need) : need;
+    if (lane == 0) *sp = now;
+    uint8_t* page = (w ? p.code[1] : p.code[0]) + (((int64_t)pg << page_log2) * p.Hkv + h) * D;
+    const int64_t row = (int64_t)p.Hkv * D;
+    if (first > 0 && now != was)
+        round_again<D / 8>(page, row, first * (D / 8), __fdiv_rn(was, now), lane, 32);
+    const float inv = exact_inverse(now);
+    uint32_t o = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        o |= (inv != 0.f && raw < 0x7f80u ? codes_of(v[i], inv) : any_codes_of(v[i], now)) << (16 * i);
+    uint8_t* out = page + first * row + 2 * W * lane;
+    if (W == 2) *reinterpret_cast<uint32_t*>(out) = o;
+    else *reinterpret_cast<uint16_t*>(out) = (uint16_t)o;
 }
 
 // ------------------------------------------------------------------ attention

@@ -92,8 +92,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         const int i = e % per, h = e / per % H, t = e / (per * H);
         const int w = h >= p.H[0];
         const int hh = w ? h - p.H[0] : h;
-        const TI* x = static_cast<const TI*>(p.x[w]) + (t0 + t) * p.xs[w] + (int64_t)hh * p.d;
-        TO* y = static_cast<TO*>(p.y[w]) + (t0 + t) * p.ys[w] + (int64_t)hh * p.d;
+        const TI* x = static_cast<const TI*>((w ? p.x[1] : p.x[0])) + (t0 + t) * (w ? p.xs[1] : p.xs[0]) + (int64_t)hh * p.d;
+        TO* y = static_cast<TO*>((w ? p.y[1] : p.y[0])) + (t0 + t) * (w ? p.ys[1] : p.ys[0]) + (int64_t)hh * p.d;
         int a, b;
         if (i < half) {
             a = p.off + (p.interleaved ? 2 * i : i);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
     }
     auto in = [&](int t, int h) {
         const int w = h >= p.H[0];
-        return static_cast<const TI*>(p.x[w]) + (t0 + t) * p.xs[w] +
+        return static_cast<const TI*>((w ? p.x[1] : p.x[0])) + (t0 + t) * (w ? p.xs[1] : p.xs[0]) +
                (int64_t)(w ? h - p.H[0] : h) * p.d;
     };
     auto turn = [&](int t, int h, float (&a)[8], float (&b)[8]) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
             b[j] *= p.out_scale;
         }
         const int w = h >= p.H[0];
-        TO* y = static_cast<TO*>(p.y[w]) + (t0 + t) * p.ys[w] + (int64_t)(w ? h - p.H[0] : h) * p.d;
+        TO* y = static_cast<TO*>((w ? p.y[1] : p.y[0])) + (t0 + t) * (w ? p.ys[1] : p.ys[0]) + (int64_t)(w ? h - p.H[0] : h) * p.d;
         store8(y + ea, a);
         store8(y + eb, b);
     };
