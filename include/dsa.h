@@ -588,7 +588,7 @@ DSA_API dsa_status_t dsa_rope_freqs(int rot, double base, int scaling, double fa
  *                            stride), and must not overlap them otherwise
  * d, offset, rot even, offset + rot <= d <= 1024, Hq + Hk <= 1024.  Pointers
  * aligned to their elements suffice; 16-byte alignment of pointers and
- * strides and d, offset and rot multiples of 16 run fastest.  L = 0 does
+ * strides and d, offset and rot multiples of 16 (F32: 8) run fastest.  L = 0 does
  * nothing.
  */
 DSA_API dsa_status_t dsa_rope(const void* q, const void* k, const int64_t* positions,

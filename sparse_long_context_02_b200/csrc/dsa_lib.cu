@@ -1387,16 +1387,16 @@ int type_bytes(int type) {
 
 template <typename TI, typename TO>
 dsa_status_t launch_rope(const char* fn, dsa::rope::Params p, cudaStream_t st) {
-    bool vec = p.d % 16 == 0 && p.off % 16 == 0 && p.rot % 16 == 0;
+    constexpr int unit = 2 * dsa::rope::kPiece<TI>;
+    bool vec = p.d % unit == 0 && p.off % unit == 0 && p.rot % unit == 0;
     for (int w = 0; w < 2; ++w)
         if (p.H[w] > 0)
             vec = vec && aligned16(p.x[w]) && aligned16(p.y[w]) &&
-                  p.xs[w] * (int64_t)sizeof(TI) % 16 == 0 && p.ys[w] * (int64_t)sizeof(TO) % 8 == 0 &&
-                  (sizeof(TO) == 1 || p.ys[w] * (int64_t)sizeof(TO) % 16 == 0);
-    // tokens per CTA: enough rows for a few rounds of every thread, while four
-    // CTAs per SM are left and the angles fit in 32 KB
-    const int64_t row = ((int64_t)(p.H[0] + p.H[1]) * p.d + 15) / 16;
-    int64_t n = p.L / (4 * num_sms());
+                  p.xs[w] * (int64_t)sizeof(TI) % 16 == 0 && p.ys[w] * (int64_t)sizeof(TO) % 16 == 0;
+    // tokens per CTA: enough rows for a few rounds of every thread, while six
+    // waves of four CTAs per SM are left and the angles fit in 32 KB
+    const int64_t row = ((int64_t)(p.H[0] + p.H[1]) * p.d + unit - 1) / unit;
+    int64_t n = p.L / (24 * num_sms());
     const int64_t most = 2304 / row, fit = 32768 / (p.rot * 4);
     n = n < most ? n : most;
     n = n < fit ? n : fit;

@@ -115,9 +115,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     }
 }
 
-// Eight consecutive elements, in 16-byte pieces (8 for e4m3).
-__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p) {
-    const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
+// E elements of one 16-byte load: 8 of bf16, 4 of fp32.
+template <typename T>
+constexpr int kPiece = 16 / sizeof(T);
+
+__device__ __forceinline__ void unpack(float (&v)[8], uint4 q) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -126,84 +128,134 @@ __device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* p) {
     }
 }
 
-__device__ __forceinline__ void load8(float (&v)[8], const float* p) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(p) + j);
-        v[4 * j] = q.x; v[4 * j + 1] = q.y; v[4 * j + 2] = q.z; v[4 * j + 3] = q.w;
-    }
+__device__ __forceinline__ void unpack(float (&v)[4], uint4 q) {
+    v[0] = __uint_as_float(q.x);
+    v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z);
+    v[3] = __uint_as_float(q.w);
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    uint32_t w[4];
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N]) {
+    if constexpr (N == 4) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (N == 2) *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    if constexpr (N == 1) *static_cast<uint32_t*>(p) = w[0];
+}
+
+template <int E>
+__device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[E]) {
+    uint32_t w[E / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < E / 2; ++j) {
         const __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
         w[j] = *reinterpret_cast<const uint32_t*>(&r);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    store_words(p, w);
 }
 
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+template <int E>
+__device__ __forceinline__ void store(float* p, const float (&v)[E]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < E / 4; ++j)
         reinterpret_cast<float4*>(p)[j] =
             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
-__device__ __forceinline__ void store8(__nv_fp8_e4m3* p, const float (&v)[8]) {
-    uint32_t w[2] = {0, 0};
+template <int E>
+__device__ __forceinline__ void store(__nv_fp8_e4m3* p, const float (&v)[E]) {
+    uint32_t w[E / 4] = {};
+    float top = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        w[j >> 2] |= (uint32_t)from_f32<__nv_fp8_e4m3>(v[j]).__x << (8 * (j & 3));
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    for (int j = 0; j < E; ++j) top = fmaxf(top, fabsf(v[j]));
+    if (top < INFINITY) {  // no infinity among them: two at a time
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) {
+            uint16_t r;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+                : "=h"(r)
+                : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+            w[j >> 1] |= (uint32_t)r << (16 * (j & 1));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            w[j >> 2] |= (uint32_t)from_f32<__nv_fp8_e4m3>(v[j]).__x << (8 * (j & 3));
+    }
+    store_words(p, w);
 }
 
-// Heads of 16-element units (d, off and rot multiples of 16, 16-byte aligned
-// rows): a thread keeps one unit u of the head, two pieces of 8 elements, and
-// walks over (token, head) rows, two at a time so that four (fp32: eight)
-// 16-byte loads are in flight.  Units [0, rot / 16) hold 8 pairs each (pieces at
-// off + 8 u and off + rot / 2 + 8 u, or 16 u and 16 u + 8), the others pass through.
+// Heads of units of 2 E elements (d, off and rot multiples of 2 E, 16-byte
+// aligned rows): a thread keeps one unit u of the head, two pieces of E elements,
+// and walks over (token, head) rows, the next row's two 16-byte loads under way
+// while it computes.  Units [0, rot / 2 E) hold E pairs each (pieces at off + E u and
+// off + rot / 2 + E u, or 2 E u and 2 E u + E), the others pass through.
 // The (cos, sin) of a token's pairs lie as [2 pairs of the unit][unit], so that
 // the 8 threads of a 128-byte shared access read neighbours.
+// Bound by memory; what counts is how many loads a multiprocessor has in flight.
+// 32768 tokens of 36 heads x 128 in bf16 take 98.9 us, 6.1 TB/s; with two rows at a
+// time 105.0, two and the next two under way (3 CTAs instead of 5) 105.2.
 template <typename TI, typename TO, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
-    extern __shared__ float4 cs4[];  // [tokens][4][rot / 16]
+    constexpr int E = kPiece<TI>;
+    extern __shared__ float4 cs4[];  // [tokens][E / 2][rot / 2 E]
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)(p.L - t0 < p.tokens ? p.L - t0 : p.tokens);
-    const int half = p.rot / 2, ru = p.rot / 16;
+    const int half = p.rot / 2, ru = half / E;
     for (int e = threadIdx.x; e < nt * half; e += kThreads) {
         const int t = e / half, i = e % half;
-        reinterpret_cast<float2*>(cs4)[((t * 4 + (i & 7) / 2) * ru + (i >> 3)) * 2 + (i & 1)] =
+        reinterpret_cast<float2*>(cs4)[((t * (E / 2) + i % E / 2) * ru + i / E) * 2 + (i & 1)] =
             angle(p, t0 + t, i);
     }
     __syncthreads();
-    const int units = p.d / 16, per = kThreads / units, H = p.H[0] + p.H[1];
+    const int units = p.d / (2 * E), per = kThreads / units, H = p.H[0] + p.H[1];
     const int u = threadIdx.x % units;
     if ((int)threadIdx.x >= per * units) return;
     int ea, eb;
     if (u < ru) {
-        ea = p.off + (INTER ? 16 * u : 8 * u);
-        eb = ea + (INTER ? 8 : half);
+        ea = p.off + (INTER ? 2 * E * u : E * u);
+        eb = ea + (INTER ? E : half);
     } else {
-        ea = 16 * (u - ru);
+        ea = 2 * E * (u - ru);
         if (ea >= p.off) ea += p.rot;
-        eb = ea + 8;
+        eb = ea + E;
     }
-    auto in = [&](int t, int h) {
-        const int w = h >= p.H[0];
-        return static_cast<const TI*>((w ? p.x[1] : p.x[0])) + (t0 + t) * (w ? p.xs[1] : p.xs[0]) +
-               (int64_t)(w ? h - p.H[0] : h) * p.d;
+    struct Row {
+        uint4 a, b;
+        int t, h;
     };
-    auto turn = [&](int t, int h, float (&a)[8], float (&b)[8]) {
+    int t = 0, h = threadIdx.x / units - per;
+    auto fetch = [&](Row& r) {
+        h += per;
+        while (h >= H) {
+            h -= H;
+            ++t;
+        }
+        r.t = t;
+        r.h = h;
+        if (t < nt) {
+            const bool w = h >= p.H[0];
+            const TI* x = static_cast<const TI*>(w ? p.x[1] : p.x[0]) +
+                          (t0 + t) * (w ? p.xs[1] : p.xs[0]) + (w ? h - p.H[0] : h) * p.d;
+            r.a = __ldcs(reinterpret_cast<const uint4*>(x + ea));
+            r.b = __ldcs(reinterpret_cast<const uint4*>(x + eb));
+        }
+    };
+    Row r;
+    fetch(r);
+    while (r.t < nt) {
+        Row next;
+        fetch(next);
+        float a[E], b[E];
+        unpack(a, r.a);
+        unpack(b, r.b);
         if (u < ru) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 c = cs4[(t * 4 + j) * ru + u];
-                float& a0 = INTER ? (j < 2 ? a[4 * j] : b[4 * j - 8]) : a[2 * j];
-                float& b0 = INTER ? (j < 2 ? a[4 * j + 1] : b[4 * j - 7]) : b[2 * j];
-                float& a1 = INTER ? (j < 2 ? a[4 * j + 2] : b[4 * j - 6]) : a[2 * j + 1];
-                float& b1 = INTER ? (j < 2 ? a[4 * j + 3] : b[4 * j - 5]) : b[2 * j + 1];
+            for (int j = 0; j < E / 2; ++j) {
+                const float4 c = cs4[(r.t * (E / 2) + j) * ru + u];
+                float& a0 = INTER ? (4 * j < E ? a[4 * j % E] : b[4 * j % E]) : a[2 * j];
+                float& b0 = INTER ? (4 * j < E ? a[4 * j % E + 1] : b[4 * j % E + 1]) : b[2 * j];
+                float& a1 = INTER ? (4 * j < E ? a[4 * j % E + 2] : b[4 * j % E + 2]) : a[2 * j + 1];
+                float& b1 = INTER ? (4 * j < E ? a[4 * j % E + 3] : b[4 * j % E + 3]) : b[2 * j + 1];
                 const float r0 = a0 * c.x - b0 * c.y, r1 = a1 * c.z - b1 * c.w;
                 b0 = b0 * c.x + a0 * c.y;
                 b1 = b1 * c.z + a1 * c.w;
@@ -212,43 +264,16 @@ __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < E; ++j) {
             a[j] *= p.out_scale;
             b[j] *= p.out_scale;
         }
-        const int w = h >= p.H[0];
-        TO* y = static_cast<TO*>((w ? p.y[1] : p.y[0])) + (t0 + t) * (w ? p.ys[1] : p.ys[0]) + (int64_t)(w ? h - p.H[0] : h) * p.d;
-        store8(y + ea, a);
-        store8(y + eb, b);
-    };
-    int t = 0, h = threadIdx.x / units;
-    auto next = [&] {
-        h += per;
-        while (h >= H) {
-            h -= H;
-            ++t;
-        }
-    };
-    h -= per;
-    next();
-    while (t < nt) {
-        float a0[8], b0[8], a1[8], b1[8];
-        const int tt = t, hh = h;
-        const TI* x = in(t, h);
-        load8(a0, x + ea);
-        load8(b0, x + eb);
-        next();
-        const bool two = t < nt;
-        if (two) {
-            x = in(t, h);
-            load8(a1, x + ea);
-            load8(b1, x + eb);
-        }
-        turn(tt, hh, a0, b0);
-        if (two) {
-            turn(t, h, a1, b1);
-            next();
-        }
+        const bool w = r.h >= p.H[0];
+        TO* y = static_cast<TO*>(w ? p.y[1] : p.y[0]) + (t0 + r.t) * (w ? p.ys[1] : p.ys[0]) +
+                (w ? r.h - p.H[0] : r.h) * p.d;
+        store(y + ea, a);
+        store(y + eb, b);
+        r = next;
     }
 }
 
