@@ -1643,7 +1643,7 @@ dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int 
         CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
         if (dev <= 63) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    kern<<<dim3((unsigned)ctas, (unsigned)(p.Hkv / HG)), kv::kAttnThreads, C::SMEM, st>>>(
+    kern<<<dim3((unsigned)ctas, (unsigned)(p.Hkv / HG)), C::THREADS, C::SMEM, st>>>(
         p, maps[0], maps[1]);
     CUDA_TRY(cudaGetLastError());
     if (merge) {

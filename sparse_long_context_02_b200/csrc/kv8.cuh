@@ -340,8 +340,6 @@ struct AttnParams {
 };
 
 constexpr int kConsumers = 8;    // consumer warps
-constexpr int kProducers = 4;    // producer warps
-constexpr int kAttnThreads = (kConsumers + kProducers) * 32;
 constexpr int kKeys = 32;        // keys of one unit: a stage of the ring
 constexpr int kMaxScan = 512;    // rows whose lengths a CTA adds up itself
 constexpr float kWeightLog2 = 15.f;                // the largest fp16 weight is 2^15
@@ -353,14 +351,16 @@ struct AttnCfg {
     static constexpr int BOX = kKeys * D;               // one head's K (or V) codes of a unit
     static constexpr int STAGE = 2 * HG * BOX;
     static constexpr int FIT = 4 * 32768 / STAGE;
-    static constexpr int STAGES = FIT < 16 ? FIT : 16;
+    static constexpr int STAGES = FIT == 4 ? 6 : FIT < 16 ? FIT : 16;
+    static constexpr int PRODUCERS = FIT == 4 ? 3 : 4;  // producer warps
+    static constexpr int THREADS = (kConsumers + PRODUCERS) * 32;
     // A stage always belongs to the same producer warp and the same consumers: a barrier's
     // parity only tells neighbouring phases apart, so whoever waits for a phase has to have
     // waited for (or caused) the one before it.
-    static_assert(STAGES % kProducers == 0 && STAGES % NSUB == 0, "");
+    static_assert(STAGES % PRODUCERS == 0 && STAGES % NSUB == 0, "");
     static constexpr int OROW = D + 4;
     static constexpr int O_AT = STAGES * STAGE;
-    static constexpr int SC_AT = O_AT + kConsumers * 8 * OROW * 4;
+    static constexpr int SC_AT = O_AT + (kConsumers - HG) * 8 * OROW * 4;
     static constexpr int M_AT = SC_AT + STAGES * HG * kKeys * 8;
     static constexpr int SCAN_AT = M_AT + kConsumers * 8 * 16;
     static constexpr int BAR_AT = SCAN_AT + (kMaxScan + 2) * 8;
@@ -516,7 +516,7 @@ struct Walk {
 };
 
 // Attention of rows over cached keys.  A CTA serves HG neighbouring KV heads of
-// its range of units (32 keys of one row): four producer warps bring units into
+// its range of units (32 keys of one row): the producer warps bring units into
 // a ring of shared-memory stages, eight consumer warps compute, HG of them, one
 // per head, at each unit, the others at the units between.
 //
@@ -550,7 +550,7 @@ struct Walk {
 // down to 2^-29 of the largest, and 2^-40 of it below, so that a long tail of
 // small weights (2^18 keys and more) still counts.
 template <int D, int HG, bool DENSE>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(AttnCfg<D, HG>::THREADS, 1)
 attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mv) {
     using C = AttnCfg<D, HG>;
@@ -577,7 +577,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         fence_mbar_init();
     }
     if (DENSE && !p.whole_rows) {
-        for (int t = threadIdx.x; t < p.rows.n; t += kAttnThreads) scan[t + 1] = row_units(p, t);
+        for (int t = threadIdx.x; t < p.rows.n; t += C::THREADS) scan[t + 1] = row_units(p, t);
         __syncthreads();
         if (warp == 0) {
             int64_t base = 0;
@@ -603,7 +603,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         // ------------------------------------------------ producers
         const int pw = warp - kConsumers;
         const int64_t rb = (int64_t)p.Hkv * D;
-        int i = pw;                    // this warp's units: pw, pw + kProducers, ...
+        int i = pw;                    // this warp's units: pw, pw + C::PRODUCERS, ...
         int64_t u = w.a + pw;          // the unit inside row w.t
         int issued = -1;
         int64_t total = w.b - w.a;     // units of the rows so far
@@ -661,7 +661,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             const int32_t slot = (int32_t)key & ((1 << p.page_log2) - 1);
             const int32_t row = (int32_t)((uint32_t)pg << p.page_log2) + slot;  // below 2^31
             const bool valid = pg >= 0;
-            u += kProducers;
+            u += C::PRODUCERS;
             more = settle();
             const int64_t key2 = more ? entry(w.t, u) : -1;
 
@@ -722,13 +722,13 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                 if (lane == 0) mbar_arrive(fb);
             }
             issued = i;
-            i += kProducers;
+            i += C::PRODUCERS;
             key = key2;
             pg = page_of(key);
         }
         // copies in flight end before the CTA does (earlier units' stages were taken again)
         if (lane == 0)
-            for (int j = issued; j >= 0 && j + C::STAGES >= total; j -= kProducers)
+            for (int j = issued; j >= 0 && j + C::STAGES >= total; j -= C::PRODUCERS)
                 if (!mbar_wait_to(p.err, smem_u32(&full[j % C::STAGES]), (j / C::STAGES) & 1)) break;
         return;
     }
@@ -925,18 +925,23 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-        named_bar_sync(1, kConsumers * 32);  // the row before has been read
+        constexpr int DT = 2 * MT;  // d of a thread: DT g .. DT g + DT - 1, o[i][c] and o[i][c + 2]
+        if (C::NSUB > 1) {
+            named_bar_sync(1, kConsumers * 32);  // the row before has been read
+            if (sub > 0) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float* q = o_s + (warp * 8 + 2 * t4 + c) * C::OROW + 2 * MT * g;
+                for (int c = 0; c < 2; ++c) {
+                    float* q = o_s + ((warp - HG) * 8 + 2 * t4 + c) * C::OROW + DT * g;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {  // m tile i, rows g and g + 8: d = 2 MT g + 2 i, + 1
-                q[2 * i] = o[i][c];
-                q[2 * i + 1] = o[i][c + 2];
+                    for (int i = 0; i < MT; ++i) {
+                        q[2 * i] = o[i][c];
+                        q[2 * i + 1] = o[i][c + 2];
+                    }
+                    if (g == 0) m_s[warp * 8 + 2 * t4 + c] = make_float4(mx[c], my[c], l[c], 0.f);
+                }
             }
-            if (g == 0) m_s[warp * 8 + 2 * t4 + c] = make_float4(mx[c], my[c], l[c], 0.f);
+            named_bar_sync(1, kConsumers * 32);
         }
-        named_bar_sync(1, kConsumers * 32);
         const bool whole = w.a == 0 && w.b == w.all;
         if (p.part_row != nullptr && threadIdx.x == 0 && blockIdx.y == 0 && w.a == 0) {
             // for the merge: the CTAs of this row, named by the one that has its first unit
@@ -950,39 +955,73 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             else
                 last = r;
         }
+        if (sub > 0) continue;
         bool write = true;
         if (whole && p.rows.off != nullptr)
             write = w.t >= p.rows.off[0] && w.t < p.rows.off[p.rows.B];
-        for (int e = threadIdx.x; write && e < HG * p.G * D; e += kConsumers * 32) {
-            const int hq = e / D, d = e % D;
-            const int hl = hq / p.G, hh = hq % p.G;
-            float Mx = -INFINITY, My = -INFINITY;
+        const int64_t Hq = (int64_t)p.Hkv * p.G;
 #pragma unroll
-            for (int v = 0; v < C::NSUB; ++v) {
-                const float4 m = m_s[(v * HG + hl) * 8 + hh];
+        for (int c = 0; c < 2; ++c) {
+            const int hh = 2 * t4 + c;
+            if (!write || hh >= p.G) continue;
+            float Mx = mx[c], My = my[c];
+#pragma unroll
+            for (int v = 1; v < C::NSUB; ++v) {
+                const float4 m = m_s[(v * HG + h) * 8 + hh];
                 Mx = fmaxf(Mx, m.x);
                 My = fmaxf(My, m.y);
             }
             const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
-            float ls = 0.f, acc = 0.f;
+            float ls = l[c] * ex2(mx[c] - ux);
+            const float f0 = ex2(my[c] - uy);
+            float acc[DT];
 #pragma unroll
-            for (int v = 0; v < C::NSUB; ++v) {
-                const float4 m = m_s[(v * HG + hl) * 8 + hh];
-                ls += m.z * ex2(m.x - ux);
-                acc += o_s[((v * HG + hl) * 8 + hh) * C::OROW + d] * ex2(m.y - uy);
+            for (int i = 0; i < MT; ++i) {
+                acc[2 * i] = o[i][c] * f0;
+                acc[2 * i + 1] = o[i][c + 2] * f0;
             }
-            const int64_t head = (int64_t)h0 * p.G + hq;
-            const int64_t Hq = (int64_t)p.Hkv * p.G;
+#pragma unroll
+            for (int v = 1; v < C::NSUB; ++v) {
+                const float4 m = m_s[(v * HG + h) * 8 + hh];
+                ls += m.z * ex2(m.x - ux);
+                const float f = ex2(m.y - uy);
+                const float4* q = reinterpret_cast<const float4*>(
+                    o_s + (((v - 1) * HG + h) * 8 + hh) * C::OROW + DT * g);
+#pragma unroll
+                for (int i = 0; i < DT / 4; ++i) {
+                    const float4 a = q[i];
+                    acc[4 * i] += a.x * f;
+                    acc[4 * i + 1] += a.y * f;
+                    acc[4 * i + 2] += a.z * f;
+                    acc[4 * i + 3] += a.w * f;
+                }
+            }
+            const int64_t head = (int64_t)(h0 + h) * p.G + hh;
             if (whole) {
-                p.O[(w.t * Hq + head) * D + d] =
-                    __float2bfloat16_rn(ls == 0.f ? 0.f : acc / ls * kWeightScale * ex2(My - Mx));
-                if (p.lse != nullptr && d == 0)
+                const float f = ls == 0.f ? 0.f : kWeightScale / ls, e = ex2(My - Mx);
+                uint4* out = reinterpret_cast<uint4*>(p.O + (w.t * Hq + head) * D + DT * g);
+#pragma unroll
+                for (int i = 0; i < DT / 8; ++i) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(
+                            ls == 0.f ? 0.f : acc[8 * i + 2 * j] * f * e,
+                            ls == 0.f ? 0.f : acc[8 * i + 2 * j + 1] * f * e);
+                        v[j] = *reinterpret_cast<const uint32_t*>(&b);
+                    }
+                    out[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                if (p.lse != nullptr && g == 0)
                     p.lse[w.t * Hq + head] = ls == 0.f ? -INFINITY
                                                        : (Mx + log2f(ls)) * 0.6931471805599453f;
             } else {
                 const int64_t at = ((int64_t)blockIdx.x * 2 + (w.a > 0 ? 0 : 1)) * Hq + head;
-                p.part_o[at * D + d] = acc;
-                if (d == 0)
+                float4* out = reinterpret_cast<float4*>(p.part_o + at * D + DT * g);
+#pragma unroll
+                for (int i = 0; i < DT / 4; ++i)
+                    out[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                if (g == 0)
                     *reinterpret_cast<float4*>(p.part_m + at * 4) = make_float4(Mx, My, ls, 0.f);
             }
         }
