@@ -1581,21 +1581,35 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
     return launch_append<128, D>(fn, p, units, st);
 }
 
-// How a launch divides: KV heads per CTA, CTAs per group of heads, bytes of the
-// partial results.  One CTA per SM in all, and none with fewer than two units
-// (one row of 2048 selected keys took 12.2, 11.7, 12.4 and 15.0 us with 1, 2, 4
-// and 8; three rows of up to 300 keys 7.6, 7.7, 9.4 and 12.1).
+// How a launch divides: KV heads per CTA, CTAs per row (0: rows are cut anywhere),
+// CTAs per group of heads, bytes of the partial results.
 struct Kv8Plan {
-    int hg, ctas;
+    int hg, cluster, ctas;
     size_t part_o, part_m, total;
 };
 
 Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
     Kv8Plan pl{};
+    const int64_t sms = num_sms();
+    const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;  // units of a row
+    // Few rows of a few units: a row per cluster, joined through shared memory.
+    // One KV head per CTA then, if that still leaves the GPU half empty.
+    if (T <= sms) {
+        int hg = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1, n = 8;
+        while (n > 1 && (n > per || T * (Hkv / hg) * n > sms)) n /= 2;
+        while (hg > 1 && T * (Hkv / hg) * n * 2 <= sms) hg /= 2;
+        if (T * (Hkv / hg) * n <= sms && per <= (int64_t)16 * n) {
+            pl.hg = hg;
+            pl.cluster = n;
+            pl.ctas = (int)T * n;
+            return pl;
+        }
+    }
+    // Otherwise one CTA per SM in all, none with fewer than two units, the rows cut
+    // into equal ranges and joined by a second kernel.
     pl.hg = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    int64_t most = num_sms() / (Hkv / pl.hg);
+    int64_t most = sms / (Hkv / pl.hg);
     most = most < dsa::kv8::kMaxParts ? most : dsa::kv8::kMaxParts;
-    const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;
     const int64_t want = T > (int64_t(1) << 40) / per ? most : T * per / 2;
     pl.ctas = (int)(want < 1 ? 1 : want < most ? want : most);
     if (pl.ctas > 1) {
@@ -1643,8 +1657,18 @@ dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int 
         CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
         if (dev <= 63) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
-    kern<<<dim3((unsigned)ctas, (unsigned)(p.Hkv / HG)), C::THREADS, C::SMEM, st>>>(
-        p, maps[0], maps[1]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.Hkv / HG));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster > 1 ? p.cluster : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1;
+    CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, maps[0], maps[1]));
     CUDA_TRY(cudaGetLastError());
     if (merge) {
         const int64_t n = p.rows.n < ctas ? p.rows.n : ctas;
@@ -1725,10 +1749,11 @@ dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const v
     p.pages = num_pages;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.vec_scales = aligned16(k_scale) && aligned16(v_scale);
-    p.whole_rows = !sparse && T > dsa::kv8::kMaxScan;
+    p.cluster = pl.cluster;
+    p.whole_rows = pl.cluster == 0 && !sparse && T > dsa::kv8::kMaxScan;
     p.O = static_cast<__nv_bfloat16*>(O);
     p.lse = lse;
-    const bool merge = pl.ctas > 1 && !p.whole_rows;
+    const bool merge = pl.total > 0 && !p.whole_rows;
     if (merge) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.part_o = reinterpret_cast<float*>(ws);

@@ -329,6 +329,7 @@ struct AttnParams {
     int64_t pages;
     float scale_log2;            // softmax scale * log2(e)
     int whole_rows;              // every key: rows are dealt out whole
+    int cluster;                 // > 0: a row is a cluster's, of that many CTAs
     __nv_bfloat16* O;            // [T][Hq][d]
     float* lse;                  // [T][Hq] or null
     // Rows that several CTAs share, per (CTA, its first or its last row, head): sums of
@@ -362,7 +363,7 @@ struct AttnCfg {
     static constexpr int O_AT = STAGES * STAGE;
     static constexpr int SC_AT = O_AT + (kConsumers - HG) * 8 * OROW * 4;
     static constexpr int M_AT = SC_AT + STAGES * HG * kKeys * 8;
-    static constexpr int SCAN_AT = M_AT + kConsumers * 8 * 16;
+    static constexpr int SCAN_AT = M_AT + (kConsumers + HG) * 8 * 16;
     static constexpr int BAR_AT = SCAN_AT + (kMaxScan + 2) * 8;
     static constexpr int SMEM = BAR_AT + STAGES * 20;
 };
@@ -453,7 +454,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 
 // The rows and units of one CTA, in order.  The units of all rows, laid end to
 // end, are cut into equal ranges, one per CTA (whole_rows: CTA c takes the rows
-// c, c + C, ...).  Every warp walks by itself.
+// c, c + C, ...; cluster: the CTAs of a cluster share one row).  Every warp walks
+// by itself.
 struct Walk {
     int64_t t;           // row
     int64_t a, b, all;   // this CTA's units [a, b) of the row's [0, all)
@@ -462,11 +464,19 @@ struct Walk {
 
     template <bool DENSE>
     __device__ __forceinline__ void open(const AttnParams& p, const int64_t* scan) {
+        left = 0;
+        if (p.cluster > 0) {
+            t = blockIdx.x / p.cluster;
+            const int64_t r = blockIdx.x % p.cluster;
+            all = DENSE ? row_units(p, t) : (p.k + kKeys - 1) / kKeys;
+            a = all * r / p.cluster;
+            b = all * (r + 1) / p.cluster;
+            return;
+        }
         if (DENSE && p.whole_rows) {
             t = blockIdx.x;
             a = 0;
             b = all = t < p.rows.n ? row_units(p, t) : 0;
-            left = 0;
             return;
         }
         const int64_t per = (p.k + kKeys - 1) / kKeys;
@@ -515,6 +525,75 @@ struct Walk {
     }
 };
 
+// Joins the row of a cluster: every CTA's sums lie in its shared memory, [HG][8][D]
+// at its start and (Mx, My, l) in row_s; CTA r writes every cluster-th piece.
+template <int D, int HG>
+__device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t* smem,
+                                              const float4* row_s, int h0) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+    const int n = p.cluster, rank = blockIdx.x % n;
+    const int64_t t = blockIdx.x / n, Hq = (int64_t)p.Hkv * p.G;
+    const bool write =
+        p.rows.off == nullptr || (t >= p.rows.off[0] && t < p.rows.off[p.rows.B]);
+    auto remote = [&](const void* q, int r) {
+        uint32_t a;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(q)), "r"(r));
+        float4 v;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(a)
+                     : "memory");
+        return v;
+    };
+    const int pieces = HG * p.G * (D / 4);
+    for (int e = threadIdx.x * n + rank; write && e < pieces; e += kConsumers * 32 * n) {
+        const int hq = e / (D / 4), c = e % (D / 4);
+        const int at = hq / p.G * 8 + hq % p.G;
+        float4 m[8], v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < n) {
+                m[r] = remote(row_s + at, r);
+                v[r] = remote(smem + (at * (D / 4) + c) * 16, r);
+            }
+        float Mx = -INFINITY, My = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < n) {
+                Mx = fmaxf(Mx, m[r].x);
+                My = fmaxf(My, m[r].y);
+            }
+        const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
+        float ls = 0.f, acc[4] = {};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < n && m[r].z != 0.f) {  // a CTA without units left no sums
+                ls += m[r].z * ex2(m[r].x - ux);
+                const float f = ex2(m[r].y - uy);
+                acc[0] += v[r].x * f;
+                acc[1] += v[r].y * f;
+                acc[2] += v[r].z * f;
+                acc[3] += v[r].w * f;
+            }
+        const float f = ls == 0.f ? 0.f : kWeightScale / ls, s = ex2(My - Mx);
+        uint32_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(ls == 0.f ? 0.f : acc[2 * j] * f * s,
+                                                           ls == 0.f ? 0.f : acc[2 * j + 1] * f * s);
+            o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        const int64_t head = (int64_t)h0 * p.G + hq;
+        *reinterpret_cast<uint2*>(p.O + (t * Hq + head) * D + 4 * c) = make_uint2(o[0], o[1]);
+        if (p.lse != nullptr && c == 0)
+            p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
+    }
+    // nobody leaves while its sums are read
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
 // Attention of rows over cached keys.  A CTA serves HG neighbouring KV heads of
 // its range of units (32 keys of one row): the producer warps bring units into
 // a ring of shared-memory stages, eight consumer warps compute, HG of them, one
@@ -562,6 +641,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
     float* o_s = reinterpret_cast<float*>(smem + C::O_AT);       // [warp][8][OROW]
     float2* sc_s = reinterpret_cast<float2*>(smem + C::SC_AT);   // [stage][HG][32]: k scale, log2 v
     float4* m_s = reinterpret_cast<float4*>(smem + C::M_AT);     // [warp][8]: Mx, My, l
+    float4* row_s = m_s + kConsumers * 8;                        // [HG][8]: the same of the row
     int64_t* scan = reinterpret_cast<int64_t*>(smem + C::SCAN_AT);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_AT);
     uint64_t* empty = full + C::STAGES;
@@ -576,7 +656,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         }
         fence_mbar_init();
     }
-    if (DENSE && !p.whole_rows) {
+    if (DENSE && !p.whole_rows && p.cluster == 0) {
         for (int t = threadIdx.x; t < p.rows.n; t += C::THREADS) scan[t + 1] = row_units(p, t);
         __syncthreads();
         if (warp == 0) {
@@ -753,6 +833,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
     int done = 0;  // units before this one
     bool ok = true;
     int2 last = make_int2(-1, -1);
+    const bool none = w.done();
     for (; !w.done(); w.next<DENSE>(p, scan)) {
         // Q, scaled by 2^qe
         uint32_t qf[NL][4][2];
@@ -955,6 +1036,10 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             else
                 last = r;
         }
+        if (p.cluster > 1) {
+            // the other heads' warps may still read the ring, where the sums go next
+            named_bar_sync(2, kConsumers * 32);
+        }
         if (sub > 0) continue;
         bool write = true;
         if (whole && p.rows.off != nullptr)
@@ -997,7 +1082,13 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                 }
             }
             const int64_t head = (int64_t)(h0 + h) * p.G + hh;
-            if (whole) {
+            if (p.cluster > 1) {
+                float4* out = reinterpret_cast<float4*>(smem) + ((h * 8 + hh) * D + DT * g) / 4;
+#pragma unroll
+                for (int i = 0; i < DT / 4; ++i)
+                    out[i] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                if (g == 0) row_s[h * 8 + hh] = make_float4(Mx, My, ls, 0.f);
+            } else if (whole) {
                 const float f = ls == 0.f ? 0.f : kWeightScale / ls, e = ex2(My - Mx);
                 uint4* out = reinterpret_cast<uint4*>(p.O + (w.t * Hq + head) * D + DT * g);
 #pragma unroll
@@ -1025,6 +1116,11 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                     *reinterpret_cast<float4*>(p.part_m + at * 4) = make_float4(Mx, My, ls, 0.f);
             }
         }
+    }
+    if (p.cluster > 1) {
+        if (none && threadIdx.x < HG * 8)
+            row_s[threadIdx.x] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        merge_cluster<D, HG>(p, smem, row_s, h0);
     }
     if (p.part_row != nullptr && threadIdx.x == 0 && blockIdx.y == 0 && p.rows.n > gridDim.x)
         p.part_row[blockIdx.x] = make_int4(last.x, (int)blockIdx.x, last.y, 0);

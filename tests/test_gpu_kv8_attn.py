@@ -295,7 +295,7 @@ def test_offsets_beyond_32_bits():
 
 def test_another_stream_and_two_captured_graphs():
     """Two graphs, each with its own workspace, replayed on two streams."""
-    c = Case([5000, 9000], 64, 32, 4, 128, 17)
+    c = Case([5000, 39000], 64, 32, 4, 128, 17)
     cache = c.cache()
     want = dsa.attn_kv8(c.Qt, *cache, c.scale)
     s = torch.cuda.Stream()

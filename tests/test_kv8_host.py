@@ -134,8 +134,8 @@ SPARSE, DENSE = CACHE + [FAKE, 64] + REST, CACHE + REST
     (22, 15, WORKSPACE), (23, FAKE + 1, INVALID)])
 def test_attention_refusals(L, at, value, status):
     a = list(SPARSE)
-    a[8], a[14] = 64, 2048  # sizes that need a workspace
-    assert L.dsa_attn_kv8_workspace_size(8, 2048, 32, 4, 128) > 15
+    a[8], a[14] = 4096, 65536  # sizes that need a workspace
+    assert L.dsa_attn_kv8_workspace_size(8, 65536, 32, 4, 128) > 15
     a[at] = value
     assert L.dsa_sparse_attn_kv8(*a) == status
     assert b"dsa_sparse_attn_kv8" in L.dsa_last_error()
