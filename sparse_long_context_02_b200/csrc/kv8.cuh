@@ -682,15 +682,15 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
     if (warp >= kConsumers) {
         // ------------------------------------------------ producers
         const int pw = warp - kConsumers;
-        const int64_t rb = (int64_t)p.Hkv * D;
-        int i = pw;                    // this warp's units: pw, pw + C::PRODUCERS, ...
-        int64_t u = w.a + pw;          // the unit inside row w.t
+        const int rb = p.Hkv * D;
+        int i = pw;                    // this warp's units: pw, pw + PRODUCERS, ...
+        int64_t u = w.a + pw;          // the unit to look at next, inside row w.t
         int issued = -1;
         int64_t total = w.b - w.a;     // units of the rows so far
         bool ok = true;
         int64_t tb = -1, n = 0;        // row of the cached lookup, its sequence and keys
         int b = 0;
-        // Advances to this warp's next unit; false at the end.
+        // Moves on to a unit of this warp; false at the end.
         auto settle = [&] {
             while (!w.done() && u >= w.b) {
                 u -= w.b;
@@ -699,51 +699,73 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             }
             return !w.done();
         };
-        auto entry = [&](int64_t t, int64_t unit) -> int64_t {
-            if (tb != t) {
-                tb = t;
-                if (!find_row(p, t, lane == 0, b, n)) n = -1;
-            }
-            const int64_t e = unit * kKeys + lane;
-            if (n < 0) return -1;
-            if (DENSE) return e < n ? e : -1;
-            return e < p.k ? (int64_t)__ldg(p.idx + t * p.k + e) : -1;
-        };
-        auto page_of = [&](int64_t key) -> int32_t {
-            if (key < 0) return -1;
-            const int32_t pg = key < n ? __ldg(p.table + (int64_t)b * p.M + (key >> p.page_log2)) : -1;
-            if (pg >= 0 && pg < p.pages) return pg;
-            record_error_to(p.err, 2);
-            return -1;
-        };
         bool more = settle();
-        int64_t key = more ? entry(w.t, u) : -1;
-        int32_t pg = page_of(key);
-        while (more && ok) {
-            // this unit's scales, and the next unit's keys, are under way while its copies go out
+        // A unit on its way: this lane's key, then its page, then the scales.  Each is asked
+        // for one turn before it is used, so that a turn waits for none of these loads (from
+        // DRAM 1 us each and dependent on each other).
+        struct Unit {
+            bool some;
+            int b;
+            int64_t n;
+            int32_t key, pg;
             float ks[HG], vs[HG];
-            {
-                const int64_t at = (int64_t)(pg < 0 ? 0 : pg) * p.Hkv + h0;
-                const float *a = p.scale[0] + at, *c = p.scale[1] + at;
-                if (HG == 4 && p.vec_scales) {
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(a));
-                    const float4 y = __ldg(reinterpret_cast<const float4*>(c));
-                    ks[0] = x.x; ks[1 % HG] = x.y; ks[2 % HG] = x.z; ks[3 % HG] = x.w;
-                    vs[0] = y.x; vs[1 % HG] = y.y; vs[2 % HG] = y.z; vs[3 % HG] = y.w;
-                } else {
-#pragma unroll
-                    for (int h = 0; h < HG; ++h) {
-                        ks[h] = __ldg(a + h);
-                        vs[h] = __ldg(c + h);
-                    }
-                }
+        };
+        auto take = [&](Unit& x) {
+            x.some = more;
+            x.key = -1;
+            if (!more) return;
+            if (tb != w.t) {
+                tb = w.t;
+                if (!find_row(p, w.t, lane == 0, b, n)) n = -1;
             }
-            const int32_t slot = (int32_t)key & ((1 << p.page_log2) - 1);
-            const int32_t row = (int32_t)((uint32_t)pg << p.page_log2) + slot;  // below 2^31
-            const bool valid = pg >= 0;
+            x.b = b;
+            x.n = n;
+            const int64_t e = u * kKeys + lane;
+            if (DENSE) {
+                if (e < n) x.key = (int32_t)e;
+            } else if (e < p.k && n >= 0) {
+                x.key = __ldg(p.idx + w.t * p.k + e);
+            }
             u += C::PRODUCERS;
             more = settle();
-            const int64_t key2 = more ? entry(w.t, u) : -1;
+        };
+        auto ask_page = [&](Unit& x) {
+            x.pg = -1;
+            if (x.key >= 0 && x.key < x.n)
+                x.pg = __ldg(p.table + (int64_t)x.b * p.M + (x.key >> p.page_log2));
+        };
+        auto ask_scales = [&](Unit& x) {
+            if (x.pg < 0 || x.pg >= p.pages) {
+                if (x.key >= 0) record_error_to(p.err, 2);
+                x.pg = -1;
+            }
+            const int64_t at = (int64_t)max(x.pg, 0) * p.Hkv + h0;
+            const float *a = p.scale[0] + at, *c = p.scale[1] + at;
+            if (HG == 4 && p.vec_scales) {
+                const float4 k = __ldg(reinterpret_cast<const float4*>(a));
+                const float4 v = __ldg(reinterpret_cast<const float4*>(c));
+                x.ks[0] = k.x; x.ks[1 % HG] = k.y; x.ks[2 % HG] = k.z; x.ks[3 % HG] = k.w;
+                x.vs[0] = v.x; x.vs[1 % HG] = v.y; x.vs[2 % HG] = v.z; x.vs[3 % HG] = v.w;
+            } else {
+#pragma unroll
+                for (int h = 0; h < HG; ++h) {
+                    x.ks[h] = __ldg(a + h);
+                    x.vs[h] = __ldg(c + h);
+                }
+            }
+        };
+        Unit now, next, after;
+        take(now);
+        take(next);
+        ask_page(now);
+        take(after);
+        ask_page(next);
+        ask_scales(now);
+        while (now.some && ok) {
+            Unit last;
+            ask_scales(next);
+            ask_page(after);
+            take(last);
 
             const int s = i % C::STAGES;
             if (i >= C::STAGES) {
@@ -753,6 +775,9 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                 ok = __shfl_sync(0xffffffffu, got, 0);
                 if (!ok) break;
             }
+            const bool valid = now.pg >= 0;
+            const int32_t row = (int32_t)((uint32_t)now.pg << p.page_log2) +
+                                (now.key & ((1 << p.page_log2) - 1));  // below 2^31
             const uint32_t bal = __ballot_sync(0xffffffffu, valid);
             const uint32_t base = smem_u32(smem + s * C::STAGE), fb = smem_u32(&full[s]);
             if constexpr (!DENSE) {
@@ -761,11 +786,12 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                     constexpr int RPI = 32 / CPR;      // rows per instruction
                     const int c = lane % CPR, r0 = lane / CPR;
                     const int hh = c / (D / 16), cc = c % (D / 16);
-                    const int64_t off = (int64_t)h0 * D + c * 16;
-                    const uint8_t *kp = p.code[0] + off, *vp = p.code[1] + off;
+                    const uint8_t* kp = p.code[0] + h0 * D + c * 16;
+                    const uint8_t* vp = p.code[1] + h0 * D + c * 16;
                     const uint32_t dst = base + hh * C::BOX;
-#pragma unroll 8
-                    for (int r = r0; r < kKeys; r += RPI) {
+#pragma unroll
+                    for (int q = 0; q < kKeys / RPI; ++q) {
+                        const int r = r0 + q * RPI;
                         const int64_t src = (int64_t)__shfl_sync(0xffffffffu, row, r) * rb;
                         const int sw = D == 128 ? cc ^ (r & 7) : cc ^ (r >> 1 & 3);
                         if (bal >> r & 1u) {
@@ -777,7 +803,8 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             }
 #pragma unroll
             for (int h = 0; h < HG; ++h)
-                sc_s[(s * HG + h) * kKeys + lane] = make_float2(ks[h], valid ? __log2f(vs[h]) : 0.f);
+                sc_s[(s * HG + h) * kKeys + lane] =
+                    make_float2(now.ks[h], valid ? __log2f(now.vs[h]) : 0.f);
             if (lane == 0) mask_s[s] = bal;
             __syncwarp();
             if constexpr (DENSE) {
@@ -803,8 +830,9 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             }
             issued = i;
             i += C::PRODUCERS;
-            key = key2;
-            pg = page_of(key);
+            now = next;
+            next = after;
+            after = last;
         }
         // copies in flight end before the CTA does (earlier units' stages were taken again)
         if (lane == 0)
