@@ -681,7 +681,7 @@ DSA_API size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int 
  *        dsa_decode_select_shard's key_out, or dsa_index_topk's rows);
  *        entries < 0 are skipped, entries >= seq_lens[b] skipped and recorded
  *        as DSA_DEVERR_INDEX
- *   O    [T][Hq][d] bf16 OUT (a row without keys is zeros)
+ *   O    [T][Hq][d] bf16 OUT (a row without keys is zeros), apart from Q
  *   lse  [T][Hq] fp32 OUT or NULL: natural log of the softmax normaliser,
  *        -inf for a row without keys
  *   workspace: dsa_attn_kv8_workspace_size(T, k, Hq, Hkv, d) bytes; calls that

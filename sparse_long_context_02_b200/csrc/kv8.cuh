@@ -525,13 +525,18 @@ struct Walk {
     }
 };
 
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
 // Joins the row of a cluster: every CTA's sums lie in its shared memory, [HG][8][D]
 // at its start and (Mx, My, l) in row_s; CTA r writes every cluster-th piece.
 template <int D, int HG>
 __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t* smem,
                                               const float4* row_s, int h0) {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    cluster_sync();
     const int n = p.cluster, rank = blockIdx.x % n;
     const int64_t t = blockIdx.x / n, Hq = (int64_t)p.Hkv * p.G;
     const bool write =
@@ -590,8 +595,7 @@ __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t
             p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
     }
     // nobody leaves while its sums are read
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    cluster_sync();
 }
 
 // Attention of rows over cached keys.  A CTA serves HG neighbouring KV heads of

@@ -10,11 +10,12 @@
 //
 // Angles.  p * w in fp32 loses the turn itself at far positions (2^-24 of
 // 262144 rad is 0.016 rad).  The table holds each frequency as a fraction of a
-// turn in units of 2^-64, so the 64-bit product p * f wraps modulo whole turns
-// by itself and its upper 32 bits, read as a signed number, are the angle in
-// units of 2^-31 half turns, good to 2^-32 turns at any position.  It goes to
-// sincospif, whose argument is in half turns, with fp32's rounding (2^-25 half
-// turns, 9e-8 rad) as the only loss.
+// turn in units of 2^-64, so the 64-bit product p * f wraps modulo whole turns by
+// itself: the angle, reduced exactly at every position.  Its distance from the
+// nearest quarter turn, at most pi / 4, goes into Taylor's series as a sum of
+// two fp32 numbers, and the series' leading terms are added last, so that cos and
+// sin, times rot_scale, come out with little more than their one rounding
+// (2^-24; sincospif on the rounded angle was off by 2e-7).
 //
 // The step only moves bytes: every element is read and written once, 36 heads
 // of 128 per token in the 32/4-head shape.  The angles (one sincospif per pair
@@ -72,9 +73,33 @@ __device__ __forceinline__ __nv_fp8_e4m3 from_f32<__nv_fp8_e4m3>(float v) {
 // cos and sin (times m) of one pair of one token.
 __device__ __forceinline__ float2 angle(const Params& p, int64_t t, int i) {
     const uint64_t turns = (uint64_t)p.pos[t] * p.freqs[i];
-    float s, c;
-    sincospif((float)(int32_t)(turns >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    return make_float2(c * p.rot_scale, p.inverse ? -s * p.rot_scale : s * p.rot_scale);
+    const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62);
+    const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));  // [-2^61, 2^61)
+    // x + y = rest * 2 pi / 2^64
+    constexpr float kTurn = 6.2831855f * 0x1p-64f, kTurnRest = -1.7484555e-7f * 0x1p-64f;
+    const float f = (float)rest, g = (float)(rest - (int64_t)f);
+    const float x = f * kTurn;
+    const float y = fmaf(f, kTurn, -x) + fmaf(f, kTurnRest, g * kTurn);
+    const float z = x * x;
+    // sin = x + ds, cos = c + dc
+    const float ds = fmaf(
+        x * z,
+        fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 39916800, 1.f / 362880), -1.f / 5040), 1.f / 120),
+             -1.f / 6),
+        y * fmaf(z, -0.5f, 1.f));
+    const float c = fmaf(z, -0.5f, 1.f);
+    const float zl = fmaf(x, x, -z) + 2.f * x * y;  // (x + y)^2 - z
+    const float dc = fmaf(
+        z * z,
+        fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 479001600, -1.f / 3628800), 1.f / 40320), -1.f / 720),
+             1.f / 24),
+        fmaf(z, -0.5f, 1.f - c) - 0.5f * zl);
+    const float m = p.rot_scale;
+    const float si = fmaf(x, m, ds * m), co = fmaf(c, m, dc * m);
+    float2 r = quarter & 1 ? make_float2(-si, co) : make_float2(co, si);
+    if (quarter & 2) r = make_float2(-r.x, -r.y);
+    if (p.inverse) r.y = -r.y;
+    return r;
 }
 
 // Any alignment, any even sizes: one pair per thread and step.

@@ -120,8 +120,8 @@ class Case:
         assert np.all(err <= tol), (np.argwhere(~(err <= tol))[:4], np.nanmax(err / (tol + 1e-30)))
         dead = n[:, 0] == 0
         assert np.all(lse[dead] == -np.inf) and np.all(O[:self.T][dead] == 0)
-        ltol = E + 2.0 ** -18 + np.abs(rl) * 2.0 ** -22
-        assert np.all(np.abs(lse - rl)[~dead] <= ltol[~dead])
+        ltol = (E + 2.0 ** -18)[~dead] + np.abs(rl[~dead]) * 2.0 ** -22
+        assert np.all(np.abs(lse[~dead] - rl[~dead]) <= ltol)
         assert dsa.device_error() == dsa.DEVERR_NONE
 
 
@@ -181,6 +181,28 @@ def test_many_rows():
     got = c.run(idx)
     c.T, c.Q, c.seq, c.seen = 800, c.Q, c.seq, c.seen
     c.check(*got, idx)
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,d,longest,k", [
+    (1, 32, 4, 128, 4000, 0), (1, 32, 4, 128, 30, 0), (2, 8, 2, 64, 5000, 300), (20, 32, 4, 128, 900, 257),
+    (74, 32, 4, 128, 300, 64), (75, 8, 4, 64, 300, 64), (148, 8, 4, 128, 200, 33), (149, 8, 4, 128, 200, 33),
+    (148, 3, 3, 64, 200, 0), (300, 8, 2, 64, 120, 0), (512, 4, 1, 128, 90, 0), (513, 4, 1, 128, 90, 0),
+    (600, 8, 4, 64, 70, 0), (600, 6, 2, 128, 70, 20), (9, 64, 64, 64, 700, 0), (5, 63, 63, 64, 200, 100)])
+def test_numbers_of_rows(T, Hq, Hkv, d, longest, k):
+    """Every way of dividing a launch: clusters of 8 to 1 CTAs per row, rows cut
+    into equal ranges (fewer and more rows than CTAs), whole rows."""
+    r = np.random.default_rng(T)
+    c = Case([int(n) for n in r.integers(0, longest + 1, T)], 16, Hq, Hkv, d, T)
+    idx = c.select(k) if k else None
+    c.check(*c.run(idx), idx)
+
+
+def test_long_chunks():
+    """600 rows of one sequence over every key (causal), and 200 rows of three."""
+    c = Case([650], 32, 8, 2, 64, 19, rows=[600])
+    c.check(*c.run())
+    c = Case([300, 40, 500], 16, 4, 1, 128, 20, rows=[100, 40, 60])
+    c.check(*c.run())
 
 
 def test_a_long_tail_of_small_weights():
@@ -288,8 +310,12 @@ def test_offsets_beyond_32_bits():
     ref, rl, mag, _, _ = KV.attention(Q, k, v, np.full((3, Hkv), 2.0 ** -6),
                                       np.full((3, Hkv), 2.0 ** -6), np.array([[0, 1, 2]]), [0],
                                       [np.arange(300)], d ** -0.5)
-    err = np.abs(O.double().cpu().numpy() - ref)
-    assert np.all(err <= mag * 2.0 ** -10 + np.abs(ref) * 2.0 ** -8)
+    idx = dev(np.arange(300, dtype=np.int32)[None])
+    S = dsa.sparse_attn_kv8(Qt, k8, v8, sc, sc, dev(np.array([use], np.int32)),
+                            dev(np.array([300], np.int32)), idx, d ** -0.5)
+    for got in (O, S):
+        err = np.abs(got.double().cpu().numpy() - ref)
+        assert np.all(err <= mag * 2.0 ** -10 + np.abs(ref) * 2.0 ** -8)
     assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-4
 
 

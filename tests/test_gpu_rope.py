@@ -1,12 +1,10 @@
 """GPU parity of the rotary positions against the float64 oracle
 (oracle/rope.py).
 
-Tolerance.  cos and sin carry the angle's fp32 rounding (2^-25 half turns,
-9.4e-8 rad), the table's truncation (2^-32 turns, 1.5e-9 rad), sincospif's own
-error (under 2 ulp, 1.2e-7) and the product with rot_scale (6e-8): 2.8e-7 of
-rot_scale; the two products and the sum add 3 * 2^-24.  Together below 2^-21
-rot_scale (|a| + |b|) for a pair (a, b), times out_scale with another 2^-24;
-then one rounding to the output's type."""
+Tolerance.  cos and sin times rot_scale are off by one rounding (2^-24) and what
+their series leave (below 2^-24 again): 2^-23 of rot_scale; the two products and
+the sum add 3 * 2^-24.  Together below 2^-21 rot_scale (|a| + |b|) for a pair (a,
+b), times out_scale with another 2^-24; then one rounding to the output's type."""
 import numpy as np
 import pytest
 import torch
@@ -180,6 +178,28 @@ def test_another_stream_and_a_captured_graph():
     again = dsa.rope(q, k, pos, f)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, again))
+
+
+def test_cos_and_sin_round_once():
+    """Pairs (1, 0) and (0, 1) read off rot_scale cos and sin: within 0.51 units
+    in the last place of rot_scale, borders of the quarter turns among the
+    angles."""
+    f = torch.tensor([1, 1 << 40, (1 << 61) - 1, 1 << 61, (1 << 61) + 1, 1 << 62, 3 << 61],
+                     dtype=torch.int64, device="cuda")
+    half = f.numel()
+    pos = torch.cat([torch.arange(-20, 4000), torch.randint(-1 << 62, 1 << 62, (20000,))]).cuda()
+    for m in (1.0, 1.2079441541679836):
+        m32 = float(np.float32(m))
+        for first, fn in ((1, np.cos), (0, np.sin)):
+            x = torch.zeros((len(pos), 1, 2 * half), device="cuda")
+            x[..., :half], x[..., half:] = first, 1 - first
+            y, _ = dsa.rope(x, None, pos, f, m)
+            turns = (pos[:, None] * f).cpu().numpy().astype(np.longdouble) / 2.0 ** 64
+            # cos of (1, 0)'s first half; sin of (0, 1)'s, negated
+            ref = m32 * fn(2 * np.longdouble(np.pi) * turns +
+                           turns * np.longdouble(2.4492935982947064e-16))
+            got = y[:, 0, :half].cpu().numpy() * (1 if first else -1)
+            assert np.abs(got - ref).max() <= 0.51 * 2.0 ** -23 * (2 if m > 1 else 1)
 
 
 def test_after_the_attention_backward():
