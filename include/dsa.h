@@ -705,7 +705,8 @@ DSA_API dsa_status_t dsa_sparse_attn_kv8(const void* Q, const void* K8, const vo
  * positions [0, seq_lens[b]), and with row_off, where the rows are the
  * sequence's last tokens, row j of R to [0, seq_lens[b] - (R - 1 - j))
  * (causal).  For layers or stages that keep the full attention, and contexts
- * no longer than the selection.  Arguments and support as
+ * no longer than the selection.  Made for single tokens and a few tokens at
+ * once: every row reads its keys anew.  Arguments and support as
  * dsa_sparse_attn_kv8, without idx; workspace for max_pages * page keys.
  */
 DSA_API dsa_status_t dsa_attn_kv8(const void* Q, const void* K8, const void* V8,

@@ -190,8 +190,9 @@ append_kernel(const AppendParams p, int units) {
     const int slot = me / C::PER_ROW, c = me % C::PER_ROW * 8;  // + ROWS i: this thread's pieces
     uint4 v[C::VPT];
     {
-        const __nv_bfloat16* x = (w ? p.x[1] : p.x[0]) + (r0 + at + slot - len) * (w ? p.xs[1] : p.xs[0]) + h * D + c;
-        const int64_t step = C::ROWS * (w ? p.xs[1] : p.xs[0]);
+        const int64_t xs = w ? p.xs[1] : p.xs[0], step = C::ROWS * xs;
+        const __nv_bfloat16* x =
+            (w ? p.x[1] : p.x[0]) + (r0 + at + slot - len) * xs + h * D + c;
 #pragma unroll
         for (int i = 0; i < C::VPT; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
@@ -265,7 +266,9 @@ append_kernel(const AppendParams p, int units) {
     else store(std::false_type{});
 }
 
-// One new token for each sequence: a warp per (sequence, K or V, head).
+// One new token for each sequence: a warp per (sequence, K or V, head), so that no
+// barrier stands in the chain of loads (length, page, scale) that is its time: 2.1 us for
+// 64 sequences of 4 x 128, against 5.9 with a block per page and head.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_one_kernel(const AppendParams p,
                                                                     int page_log2) {
@@ -278,7 +281,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_one_kernel(const Append
     if (b >= p.rows.B) return;
     const int len = __ldg(p.lens + b);
     uint32_t v[W];
-    const uint32_t* x = reinterpret_cast<const uint32_t*>((w ? p.x[1] : p.x[0]) + b * (w ? p.xs[1] : p.xs[0]) + (int64_t)h * D) + W * lane;
+    const __nv_bfloat16* head = (w ? p.x[1] : p.x[0]) + b * (w ? p.xs[1] : p.xs[0]) + h * D;
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(head) + W * lane;
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = __ldg(x + i);
     if (len < 0) return;
@@ -310,7 +314,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_one_kernel(const Append
     uint32_t o = 0;
 #pragma unroll
     for (int i = 0; i < W; ++i)
-        o |= (inv != 0.f && raw < 0x7f80u ? codes_of(v[i], inv) : any_codes_of(v[i], now)) << (16 * i);
+        o |= (inv != 0.f && raw < 0x7f80u ? codes_of(v[i], inv) : any_codes_of(v[i], now))
+             << (16 * i);
     uint8_t* out = page + first * row + 2 * W * lane;
     if (W == 2) *reinterpret_cast<uint32_t*>(out) = o;
     else *reinterpret_cast<uint16_t*>(out) = (uint16_t)o;
@@ -534,7 +539,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // Joins the row of a cluster: every CTA's sums lie in its shared memory, [HG][8][D]
-// at its start and (Mx, My, l) in row_s; CTA r writes every cluster-th piece.
+// at its start and (Mx, My, l) in row_s; CTA r writes every cluster-th piece.  Saves the
+// second kernel: one row of 2048 keys 9.3 -> 8.1 us, three rows of up to 300 keys 7.8 -> 6.1.
 template <int D, int HG>
 __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t* smem,
                                               const float4* row_s, int h0) {
@@ -601,13 +607,27 @@ __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t
 }
 
 // Attention of rows over cached keys.  A CTA serves HG neighbouring KV heads of
-// its range of units (32 keys of one row): the producer warps bring units into
-// a ring of shared-memory stages, eight consumer warps compute, HG of them, one
-// per head, at each unit, the others at the units between.
+// its range of units (32 keys of one row): three or four producer warps bring
+// units into a ring of shared-memory stages, eight consumer warps compute, HG of
+// them, one per head, at each unit, the others at the units between.
+//
+// Measured on 32/4 heads of 128 (device time).  Over every key, 8 rows of 16K to
+// 128K keys: 94.9 us, 6.06 TB/s of codes (93 % of a copy's rate), bound by HBM.  64 rows
+// of 2048 selected keys: 37.6 us with the merge, 3.6 TB/s, bound by the latency of
+// dependent loads (index row, table, scales, codes) and 512-byte pieces.  1000 rows of
+// one chunk over a cache that fits L2: 294 us, 7.1 TB/s of gathered codes; issue slots
+// are 53 % and the ALU pipe 49 % busy (widening codes takes half of it) with 11 warps per
+// SM, all that 168 registers allow; the copies alone take 234 us with four producers.
+// One row of 2048: 7.9 us, latency.  Loads straight to registers, 16 warps per SM
+// without a ring, took 242.6, 63.9, 444.9 and 11.5.
+// Tried and slower: e4m3 operands on mma.sync, which converts inside (24 cycles against
+// 8.4 for fp16's with fresh operands); V read transposed by ldmatrix b8 instead of byte
+// permutes (305 us on the chunk against 295, for want of registers); 16 consumer warps
+// (408, spills); the next unit's scores beside this one's softmax (354, holds stages).
 //
 // Copies.  Selected keys are gathered with 16-byte cp.async, a warp taking a
-// key's HG * d bytes at once (rows this short are too many for the copy
-// engine); over every key a unit lies inside a page and comes as one TMA box
+// key's HG * d bytes at once (one bulk copy for each
+// row this short keeps the copy engine from the rate that the load path reaches); over every key a unit lies inside a page and comes as one TMA box
 // per head.  Either way a head's 32 rows of d bytes lie with their 16-byte
 // pieces exclusive-or'ed by the row, as TMA's swizzle does.
 //
@@ -631,8 +651,8 @@ __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t
 // maxima are kept: Mx for l = sum 2^(x - Mx), My for the weights 2^(y - My) that
 // multiply the V codes, so the weights are at most 1 whatever the scales are:
 // O = (sum 2^(y - My) code) * 2^(My - Mx) / l.  They are held times 2^15 in fp16:
-// rounding them costs 2^-11 each, an eighth of the output's own bf16 rounding,
-// down to 2^-29 of the largest, and 2^-40 of it below, so that a long tail of
+// rounding them costs 2^-11 each, an eighth of the output's own bf16 rounding, down
+// to 2^-29 of the largest, and 2^-40 of it below, so that a long tail of
 // small weights (2^18 keys and more) still counts.
 template <int D, int HG, bool DENSE>
 __global__ void __launch_bounds__(AttnCfg<D, HG>::THREADS, 1)
@@ -1164,7 +1184,8 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
 // Merges one head of a row that several CTAs shared.  part_row has an entry (row,
 // first CTA, last CTA) or -1 per row, or per CTA where rows are more.
 // Latency decides it (a row of 148 parts is 78 KB): all maxima are loaded at
-// once, then D / 4 threads take a part, four loads in flight each.
+// once, then D / 4 threads take a part, four loads in flight each.  One row of 32 parts
+// went from 19.3 to 11.7 us in all against a thread per element walking the parts.
 constexpr int kCombineThreads = 256;
 constexpr int kMaxParts = 512;
 

@@ -102,7 +102,8 @@ __device__ __forceinline__ float2 angle(const Params& p, int64_t t, int i) {
     return r;
 }
 
-// Any alignment, any even sizes: one pair per thread and step.
+// Any alignment, any even sizes: one pair per thread and step.  Four times the time of
+// the form below (32768 tokens of 36 heads x 128: 383 us); for what that cannot take.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     extern __shared__ float2 cs[];  // [tokens][rot / 2]
@@ -117,8 +118,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         const int i = e % per, h = e / per % H, t = e / (per * H);
         const int w = h >= p.H[0];
         const int hh = w ? h - p.H[0] : h;
-        const TI* x = static_cast<const TI*>((w ? p.x[1] : p.x[0])) + (t0 + t) * (w ? p.xs[1] : p.xs[0]) + (int64_t)hh * p.d;
-        TO* y = static_cast<TO*>((w ? p.y[1] : p.y[0])) + (t0 + t) * (w ? p.ys[1] : p.ys[0]) + (int64_t)hh * p.d;
+        const TI* x = static_cast<const TI*>(w ? p.x[1] : p.x[0]) +
+                      (t0 + t) * (w ? p.xs[1] : p.xs[0]) + (int64_t)hh * p.d;
+        TO* y = static_cast<TO*>(w ? p.y[1] : p.y[0]) + (t0 + t) * (w ? p.ys[1] : p.ys[0]) +
+                (int64_t)hh * p.d;
         int a, b;
         if (i < half) {
             a = p.off + (p.interleaved ? 2 * i : i);
@@ -217,8 +220,10 @@ __device__ __forceinline__ void store(__nv_fp8_e4m3* p, const float (&v)[E]) {
 // The (cos, sin) of a token's pairs lie as [2 pairs of the unit][unit], so that
 // the 8 threads of a 128-byte shared access read neighbours.
 // Bound by memory; what counts is how many loads a multiprocessor has in flight.
-// 32768 tokens of 36 heads x 128 in bf16 take 98.9 us, 6.1 TB/s; with two rows at a
-// time 105.0, two and the next two under way (3 CTAs instead of 5) 105.2.
+// 32768 tokens of 36 heads x 128 in bf16 take 98 us, 6.2 TB/s (94 % of a copy's rate);
+// with two rows at a time and no prefetch 105.0, two and the next two under way (3
+// CTAs per SM instead of 5) 105.2.  8191 tokens in fp32: 48 us, 6.3 TB/s (8 elements
+// per unit; 16, with twice the registers, 60).  16385 x 65 heads to e4m3: 75 us, 5.5 TB/s.
 template <typename TI, typename TO, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
     constexpr int E = kPiece<TI>;

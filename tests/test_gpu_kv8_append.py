@@ -229,3 +229,11 @@ def test_another_stream_and_a_captured_graph():
             KV.append(new, c.codes[i], c.scales[i], c.table, lens, [0, 1, 2])
         lens = [n + 1 for n in lens]
         c.check()
+
+
+def test_no_rows():
+    c = Cache(3, 16, 2, 64, [[1]])
+    x = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    dsa.kv8_append(x, x, *c.dc, *c.ds, c.dt, dev(np.array([3], np.int32)), off)
+    c.check()

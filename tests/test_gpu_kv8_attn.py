@@ -184,10 +184,12 @@ def test_many_rows():
 
 
 @pytest.mark.parametrize("T,Hq,Hkv,d,longest,k", [
-    (1, 32, 4, 128, 4000, 0), (1, 32, 4, 128, 30, 0), (2, 8, 2, 64, 5000, 300), (20, 32, 4, 128, 900, 257),
-    (74, 32, 4, 128, 300, 64), (75, 8, 4, 64, 300, 64), (148, 8, 4, 128, 200, 33), (149, 8, 4, 128, 200, 33),
-    (148, 3, 3, 64, 200, 0), (300, 8, 2, 64, 120, 0), (512, 4, 1, 128, 90, 0), (513, 4, 1, 128, 90, 0),
-    (600, 8, 4, 64, 70, 0), (600, 6, 2, 128, 70, 20), (9, 64, 64, 64, 700, 0), (5, 63, 63, 64, 200, 100)])
+    (1, 32, 4, 128, 4000, 0), (1, 32, 4, 128, 30, 0), (2, 8, 2, 64, 5000, 300),
+    (20, 32, 4, 128, 900, 257), (74, 32, 4, 128, 300, 64), (75, 8, 4, 64, 300, 64),
+    (148, 8, 4, 128, 200, 33), (149, 8, 4, 128, 200, 33), (148, 3, 3, 64, 200, 0),
+    (300, 8, 2, 64, 120, 0), (512, 4, 1, 128, 90, 0), (513, 4, 1, 128, 90, 0),
+    (600, 8, 4, 64, 70, 0), (600, 6, 2, 128, 70, 20), (9, 64, 64, 64, 700, 0),
+    (5, 63, 63, 64, 200, 100)])
 def test_numbers_of_rows(T, Hq, Hkv, d, longest, k):
     """Every way of dividing a launch: clusters of 8 to 1 CTAs per row, rows cut
     into equal ranges (fewer and more rows than CTAs), whole rows."""
@@ -243,6 +245,25 @@ def test_scales_far_apart():
     q[0] *= 0
     c.set_q(q)
     c.check(*c.run())
+
+
+def test_no_rows_and_a_workspace_that_is_too_small():
+    c = Case([39000], 64, 32, 4, 128, 21)
+    cache = c.cache()
+    empty = [t[:0].contiguous() for t in cache[4:]]
+    assert dsa.attn_kv8(c.Qt[:0], *cache[:4], *empty, c.scale).shape == (0, 32, 128)
+    idx = torch.zeros((0, 5), dtype=torch.int32, device="cuda")
+    assert dsa.sparse_attn_kv8(c.Qt[:0], *cache[:4], *empty, idx, c.scale).shape == (0, 32, 128)
+    with pytest.raises(dsa.DSAError, match="workspace"):
+        dsa.attn_kv8(c.Qt, *cache, c.scale, workspace=torch.empty(64, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        dsa.attn_kv8(c.Qt.transpose(0, 1).expand(32, 2, 128).transpose(0, 1), *cache, c.scale)
+    with pytest.raises(ValueError, match="idx"):
+        dsa.sparse_attn_kv8(c.Qt, *cache, None, c.scale)
+    with pytest.raises(ValueError, match="stream"):
+        dsa.attn_kv8(c.Qt, *cache, c.scale, stream="current")
+    assert dsa.attn_kv8(c.Qt, *cache, c.scale, stream=0).shape == (1, 32, 128)
+    torch.cuda.synchronize()
 
 
 def test_nan_and_infinity_stay_in_their_rows():
