@@ -1581,6 +1581,40 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
     return launch_append<128, D>(fn, p, units, st);
 }
 
+// Clusters of n CTAs of the 8-bit attention (one CTA per SM) that run at once: fewer than
+// SMs / n, as a cluster stays within a GPC.  Asked once per device.
+int kv8_clusters(int n) {
+    namespace kv = dsa::kv8;
+    using C = kv::AttnCfg<128, 4>;
+    static std::atomic<int> known[64][4];
+    int dev = 0;
+    const int sms = num_sms(), at = n == 8 ? 3 : n == 4 ? 2 : 1;
+    if (n == 1) return sms;
+    const int guess = sms / n * 4 / 5;  // without a GPU, or an answer
+    if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) return guess;
+    int v = known[dev][at].load(std::memory_order_relaxed);
+    if (v > 0) return v;
+    auto kern = kv::attn_kernel<128, 4, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / n * n));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&v, kern, &cfg) != cudaSuccess || v < 1) {
+        cudaGetLastError();
+        v = guess;
+    }
+    known[dev][at].store(v, std::memory_order_relaxed);
+    return v;
+}
+
 // How a launch divides: KV heads per CTA, CTAs per row (0: rows are cut anywhere),
 // CTAs per group of heads, bytes of the partial results.
 struct Kv8Plan {
@@ -1592,15 +1626,19 @@ Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
     Kv8Plan pl{};
     const int64_t sms = num_sms();
     const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;  // units of a row
-    // Few rows of a few units: a row per cluster, joined through shared memory (one
-    // row of 2048 keys 8.1 us against 9.3 for ranges and a second kernel; 64 such rows, two
-    // CTAs each, 45.0 against 44.5, so longer units go the other way).  One KV head per
-    // CTA then, if that still leaves the GPU half empty.
+    // Few rows of up to 32 units per CTA: a row per cluster, joined through shared memory,
+    // which saves the second kernel and its launch (one row of 2048 keys 8.1 us against 9.3,
+    // 64 such rows 31.3 against 38, 100 of 1024 26.6 against 32).  Not longer ones: rows of
+    // very different lengths are what the equal ranges below are for.  As many CTAs per row
+    // as run at once: a second wave of clusters doubles the time (16 rows of 2048 keys in
+    // clusters of 8: 26.9 us where 15 fit, 12.6 in clusters of 4).  One KV head per CTA
+    // while that keeps to one wave.
     if (T <= sms) {
         int hg = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1, n = 8;
-        while (n > 1 && (n > per || T * (Hkv / hg) * n > sms)) n /= 2;
-        while (hg > 1 && T * (Hkv / hg) * n * 2 <= sms) hg /= 2;
-        if (T * (Hkv / hg) * n <= sms && per <= (int64_t)16 * n) {
+        while (n > 1 && (n > per || T * (Hkv / hg) > kv8_clusters(n))) n /= 2;
+        while (hg > 1 && T * (Hkv / hg) * 2 <= kv8_clusters(n)) hg /= 2;
+        const int64_t used = T * (Hkv / hg) * n;
+        if (used <= sms && per <= (int64_t)32 * n) {
             pl.hg = hg;
             pl.cluster = n;
             pl.ctas = (int)T * n;
@@ -1674,8 +1712,14 @@ dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int 
     CUDA_TRY(cudaGetLastError());
     if (merge) {
         const int64_t n = p.rows.n < ctas ? p.rows.n : ctas;
-        CUDA_TRY(launch_chained(kv::combine_kernel<D>, dim3((unsigned)n, (unsigned)(p.Hkv * p.G)),
-                                dim3(kv::kCombineThreads), 0, st, p));
+        const int Hq = p.Hkv * p.G, warps = kv::kCombineThreads / 32;
+        if (ctas <= 2 * n)  // some two parts a row, unless one is far longer than the rest
+            CUDA_TRY(launch_chained(kv::combine_few_kernel<D>,
+                                    dim3((unsigned)n, (unsigned)((Hq + warps - 1) / warps)),
+                                    dim3(kv::kCombineThreads), 0, st, p));
+        else
+            CUDA_TRY(launch_chained(kv::combine_kernel<D>, dim3((unsigned)n, (unsigned)Hq),
+                                    dim3(kv::kCombineThreads), 0, st, p));
         CUDA_TRY(cudaGetLastError());
     }
     return ok();

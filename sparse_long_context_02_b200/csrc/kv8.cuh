@@ -540,7 +540,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 // Joins the row of a cluster: every CTA's sums lie in its shared memory, [HG][8][D]
 // at its start and (Mx, My, l) in row_s; CTA r writes every cluster-th piece.  Saves the
-// second kernel: one row of 2048 keys 9.3 -> 8.1 us, three rows of up to 300 keys 7.8 -> 6.1.
+// second kernel: one row of 2048 keys 9.3 -> 8.1 us, three rows of up to 300 keys 7.8 -> 6.2.
 template <int D, int HG>
 __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t* smem,
                                               const float4* row_s, int h0) {
@@ -612,10 +612,10 @@ __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t
 // them, one per head, at each unit, the others at the units between.
 //
 // Measured on 32/4 heads of 128 (device time).  Over every key, 8 rows of 16K to
-// 128K keys: 94.9 us, 6.06 TB/s of codes (93 % of a copy's rate), bound by HBM.  64 rows
-// of 2048 selected keys: 37.6 us with the merge, 3.6 TB/s, bound by the latency of
-// dependent loads (index row, table, scales, codes) and 512-byte pieces.  1000 rows of
-// one chunk over a cache that fits L2: 294 us, 7.1 TB/s of gathered codes; issue slots
+// 128K keys: 94.6 us, 6.07 TB/s of codes (93 % of a copy's rate), bound by HBM.  64 rows
+// of 2048 selected keys: 31.3 us, 4.3 TB/s, bound by HBM's rate for 512-byte pieces (5 TB/s
+// with more rows) and a start of dependent loads (index row, table, codes).  1000 rows of
+// one chunk over a cache that fits L2: 285 us, 7.4 TB/s of gathered codes; issue slots
 // are 53 % and the ALU pipe 49 % busy (widening codes takes half of it) with 11 warps per
 // SM, all that 168 registers allow; the copies alone take 234 us with four producers.
 // One row of 2048: 7.9 us, latency.  Loads straight to registers, 16 warps per SM
@@ -1262,6 +1262,67 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const AttnPara
         if (p.lse != nullptr && threadIdx.x == 0)
             p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
     }
+}
+
+// The same for rows of few parts, as many rows leave: a warp per head, which walks over
+// them.  The chunk of 1000 rows 294 -> 285 us.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) combine_few_kernel(const AttnParams p) {
+    constexpr int E = D / 32;  // elements of a lane
+    pdl_wait();
+    const int4 r = p.part_row[blockIdx.x];
+    const int64_t Hq = (int64_t)p.Hkv * p.G;
+    const int64_t head = blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5);
+    if (r.x < 0 || head >= Hq) return;
+    const int64_t t = r.x;
+    if (p.rows.off != nullptr && (t < p.rows.off[0] || t >= p.rows.off[p.rows.B])) return;
+    const int n = r.z - r.y + 1, lane = threadIdx.x & 31;
+    auto at = [&](int j) { return ((int64_t)(r.y + j) * 2 + (j == 0 ? 1 : 0)) * Hq + head; };
+    // a part's maxima per lane
+    float Mx = -INFINITY, My = -INFINITY;
+#pragma unroll 4
+    for (int j = lane; j < n; j += 32) {
+        const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j) * 4);
+        Mx = fmaxf(Mx, m.x);
+        My = fmaxf(My, m.y);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, d));
+        My = fmaxf(My, __shfl_xor_sync(0xffffffffu, My, d));
+    }
+    const float ux = Mx == -INFINITY ? 0.f : Mx, uy = My == -INFINITY ? 0.f : My;
+    float ls = 0.f, acc[E] = {};
+    for (int j0 = 0; j0 < n; j0 += 32) {
+        const int some = n - j0 < 32 ? n - j0 : 32;
+        float g = 0.f;
+        if (lane < some) {
+            const float4 m = *reinterpret_cast<const float4*>(p.part_m + at(j0 + lane) * 4);
+            ls += m.z * ex2(m.x - ux);
+            g = ex2(m.y - uy);
+        }
+#pragma unroll 16
+        for (int j = 0; j < some; ++j) {
+            const float* q = p.part_o + at(j0 + j) * D + E * lane;
+            const float f = __shfl_sync(0xffffffffu, g, j);
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 v = *reinterpret_cast<const float2*>(q + e);
+                acc[e] += v.x * f;
+                acc[e + 1] += v.y * f;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    const float f = ls == 0.f ? 0.f : kWeightScale / ls, s = ex2(My - Mx);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<__nv_bfloat162*>(p.O + (t * Hq + head) * D + E * lane + e) =
+            __floats2bfloat162_rn(ls == 0.f ? 0.f : acc[e] * f * s,
+                                  ls == 0.f ? 0.f : acc[e + 1] * f * s);
+    if (p.lse != nullptr && lane == 0)
+        p.lse[t * Hq + head] = ls == 0.f ? -INFINITY : (Mx + log2f(ls)) * 0.6931471805599453f;
 }
 
 }  // namespace kv8
