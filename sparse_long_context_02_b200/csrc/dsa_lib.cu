@@ -105,9 +105,12 @@ int max_optin_smem() {
 }
 
 int num_sms() {
+    static std::atomic<int> known[64];  // asked once per device
     int dev = 0, v = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (v = known[dev].load(std::memory_order_relaxed)) > 0) return v;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < 64) known[dev].store(v, std::memory_order_relaxed);
     return v;
 }
 
@@ -1583,12 +1586,12 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
 
 // Clusters of n CTAs of the 8-bit attention (one CTA per SM) that run at once: fewer than
 // SMs / n, as a cluster stays within a GPC.  Asked once per device.
-int kv8_clusters(int n) {
+int kv8_clusters(int n, int sms) {
     namespace kv = dsa::kv8;
     using C = kv::AttnCfg<128, 4>;
     static std::atomic<int> known[64][4];
     int dev = 0;
-    const int sms = num_sms(), at = n == 8 ? 3 : n == 4 ? 2 : 1;
+    const int at = n == 8 ? 3 : n == 4 ? 2 : 1;
     if (n == 1) return sms;
     const int guess = sms / n * 4 / 5;  // without a GPU, or an answer
     if (cudaGetDevice(&dev) != cudaSuccess || dev > 63) return guess;
@@ -1624,7 +1627,7 @@ struct Kv8Plan {
 
 Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
     Kv8Plan pl{};
-    const int64_t sms = num_sms();
+    const int sms = num_sms();
     const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;  // units of a row
     // Few rows of up to 32 units per CTA: a row per cluster, joined through shared memory,
     // which saves the second kernel and its launch (one row of 2048 keys 8.1 us against 9.3,
@@ -1635,8 +1638,8 @@ Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
     // while that keeps to one wave.
     if (T <= sms) {
         int hg = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1, n = 8;
-        while (n > 1 && (n > per || T * (Hkv / hg) > kv8_clusters(n))) n /= 2;
-        while (hg > 1 && T * (Hkv / hg) * 2 <= kv8_clusters(n)) hg /= 2;
+        while (n > 1 && (n > per || T * (Hkv / hg) > kv8_clusters(n, sms))) n /= 2;
+        for (const int64_t fit = kv8_clusters(n, sms); hg > 1 && T * (Hkv / hg) * 2 <= fit;) hg /= 2;
         const int64_t used = T * (Hkv / hg) * n;
         if (used <= sms && per <= (int64_t)32 * n) {
             pl.hg = hg;
