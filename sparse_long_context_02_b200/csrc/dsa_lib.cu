@@ -1407,14 +1407,10 @@ dsa_status_t launch_rope(const char* fn, dsa::rope::Params p, cudaStream_t st) {
     p.tokens = (int)(n < 1 ? 1 : n);
     const int64_t grid = (p.L + p.tokens - 1) / p.tokens;
     const size_t smem = (size_t)p.tokens * (p.rot / 2) * sizeof(float2);
-    if (!vec)
-        dsa::rope::rope_kernel<TI, TO><<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
-    else if (p.interleaved)
-        dsa::rope::rope_vec_kernel<TI, TO, true>
-            <<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
-    else
-        dsa::rope::rope_vec_kernel<TI, TO, false>
-            <<<(unsigned)grid, dsa::rope::kThreads, smem, st>>>(p);
+    auto kern = !vec            ? dsa::rope::rope_kernel<TI, TO>
+                : p.interleaved ? dsa::rope::rope_vec_kernel<TI, TO, true>
+                                : dsa::rope::rope_vec_kernel<TI, TO, false>;
+    CUDA_TRY(launch_chained(kern, dim3((unsigned)grid), dim3(dsa::rope::kThreads), smem, st, p));
     CUDA_TRY(cudaGetLastError());
     return ok();
 }
@@ -1560,9 +1556,9 @@ template <int PAGE, int D>
 dsa_status_t launch_append(const char* fn, const dsa::kv8::AppendParams& p, int64_t units,
                            cudaStream_t st) {
     constexpr int TEAMS = dsa::kv8::AppendCfg<PAGE, D>::TEAMS;
-    dsa::kv8::append_kernel<PAGE, D>
-        <<<(unsigned)((units * 2 * p.Hkv + TEAMS - 1) / TEAMS), dsa::kv8::kAppendThreads, 0, st>>>(
-            p, (int)units);
+    CUDA_TRY(launch_chained(dsa::kv8::append_kernel<PAGE, D>,
+                            dim3((unsigned)((units * 2 * p.Hkv + TEAMS - 1) / TEAMS)),
+                            dim3(dsa::kv8::kAppendThreads), 0, st, p, (int)units));
     CUDA_TRY(cudaGetLastError());
     return ok();
 }
@@ -1573,8 +1569,9 @@ dsa_status_t dispatch_append(const char* fn, int page, const dsa::kv8::AppendPar
     if (p.rows.off == nullptr) {
         const int log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
         const int64_t warps = (int64_t)p.rows.B * 2 * p.Hkv, per = dsa::kv8::kAppendThreads / 32;
-        dsa::kv8::append_one_kernel<D>
-            <<<(unsigned)((warps + per - 1) / per), dsa::kv8::kAppendThreads, 0, st>>>(p, log2);
+        CUDA_TRY(launch_chained(dsa::kv8::append_one_kernel<D>,
+                                dim3((unsigned)((warps + per - 1) / per)),
+                                dim3(dsa::kv8::kAppendThreads), 0, st, p, log2));
         CUDA_TRY(cudaGetLastError());
         return ok();
     }
@@ -1705,12 +1702,14 @@ dsa_status_t launch_kv8_attn(const char* fn, const dsa::kv8::AttnParams& p, int 
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster > 1 ? p.cluster : 1;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster > 1 ? p.cluster : 1;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, p, maps[0], maps[1]));
     CUDA_TRY(cudaGetLastError());
     if (merge) {

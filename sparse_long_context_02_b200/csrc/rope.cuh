@@ -107,6 +107,7 @@ __device__ __forceinline__ float2 angle(const Params& p, int64_t t, int i) {
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     extern __shared__ float2 cs[];  // [tokens][rot / 2]
+    pdl_wait();
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)(p.L - t0 < p.tokens ? p.L - t0 : p.tokens);
     const int half = p.rot / 2;
@@ -228,6 +229,7 @@ template <typename TI, typename TO, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_vec_kernel(const Params p) {
     constexpr int E = kPiece<TI>;
     extern __shared__ float4 cs4[];  // [tokens][E / 2][rot / 2 E]
+    pdl_wait();
     const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
     const int nt = (int)(p.L - t0 < p.tokens ? p.L - t0 : p.tokens);
     const int half = p.rot / 2, ru = half / E;
