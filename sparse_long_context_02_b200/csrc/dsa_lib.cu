@@ -325,7 +325,7 @@ dsa_status_t attn_prefill_rows(const char* fn, const void* Q, const void* K, con
 
 extern "C" {
 
-int dsa_version(void) { return 100; }
+int dsa_version(void) { return 200; }
 
 const char* dsa_status_string(int status) {
     switch (status) {
