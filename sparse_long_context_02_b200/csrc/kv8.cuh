@@ -13,7 +13,10 @@
 //
 // Every kernel here is launched by programmatic dependence and waits for the ones
 // before it first thing: 2 us less between two calls (a token to each of 64
-// sequences 4.1 -> 2.9 us a call, three short rows 8.2 -> 6.5).
+// sequences 4.1 -> 2.9 us a call, three short rows 8.2 -> 6.5).  So a kernel may be
+// resident while the one before it still writes the index rows, tables or elements that
+// it will read: those are plain loads after the wait, never the read-only path, whose
+// data nobody may write while the kernel lives.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -80,7 +83,7 @@ template <int PAGE>
 __device__ __forceinline__ bool find_unit(const AppendParams& p, int u, bool report, int& b,
                                           int64_t& r0, int64_t& n, int& len, int& col) {
     const Rows& rw = p.rows;
-    auto base = [&](int i) { return max(__ldg(rw.off + i), 0) / PAGE + 2 * i; };
+    auto base = [&](int i) { return max(rw.off[i], 0) / PAGE + 2 * i; };
     int lo = 0, hi = rw.B - 1;  // the last b with base(b) <= u
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -88,9 +91,9 @@ __device__ __forceinline__ bool find_unit(const AppendParams& p, int u, bool rep
         else hi = mid - 1;
     }
     b = lo;
-    len = __ldg(p.lens + b);
-    r0 = __ldg(rw.off + b);
-    const int64_t r1 = __ldg(rw.off + b + 1);
+    len = p.lens[b];
+    r0 = rw.off[b];
+    const int64_t r1 = rw.off[b + 1];
     if (r0 < 0 || r1 < r0 || r1 > rw.n) {
         if (report) record_error_to(p.err, 2);
         return false;
@@ -205,7 +208,7 @@ append_kernel(const AppendParams p, int units) {
                 v[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * step));
         }
     }
-    const int32_t pg = live ? __ldg(p.table + (int64_t)b * p.M + col) : 0;
+    const int32_t pg = live ? p.table[(int64_t)b * p.M + col] : 0;
     if (pg < 0 || pg >= p.pages) {
         if (me == 0) record_error_to(p.err, 2);
         live = false;
@@ -285,15 +288,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_one_kernel(const Append
     const uint32_t uh = item - (uint32_t)b * 2 * hkv;
     const int w = uh >= hkv, h = uh - (w ? hkv : 0);
     if (b >= p.rows.B) return;
-    const int len = __ldg(p.lens + b);
+    const int len = p.lens[b];
     uint32_t v[W];
     const __nv_bfloat16* head = (w ? p.x[1] : p.x[0]) + b * (w ? p.xs[1] : p.xs[0]) + h * D;
     const uint32_t* x = reinterpret_cast<const uint32_t*>(head) + W * lane;
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = __ldg(x + i);
+    for (int i = 0; i < W; ++i) v[i] = x[i];
     if (len < 0) return;
     const int col = len >> page_log2, first = len & ((1 << page_log2) - 1);
-    const int32_t pg = col < p.M ? __ldg(p.table + b * p.M + col) : -1;
+    const int32_t pg = col < p.M ? p.table[b * p.M + col] : -1;
     if (pg < 0 || pg >= p.pages) {
         if (lane == 0) record_error_to(p.err, 2);
         return;
@@ -758,7 +761,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             if (DENSE) {
                 if (e < n) x.key = (int32_t)e;
             } else if (e < p.k && owned) {  // does not wait for the sequence's length
-                x.key = __ldg(p.idx + w.t * p.k + e);
+                x.key = p.idx[w.t * p.k + e];
             }
             u += C::PRODUCERS;
             more = settle();
@@ -766,7 +769,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         auto ask_page = [&](Unit& x) {
             x.pg = -1;
             if (x.key >= 0 && x.key < x.n)
-                x.pg = __ldg(p.table + (int64_t)x.b * p.M + (x.key >> p.page_log2));
+                x.pg = p.table[(int64_t)x.b * p.M + (x.key >> p.page_log2)];
         };
         auto ask_scales = [&](Unit& x) {
             if (x.pg < 0 || x.pg >= p.pages) {
@@ -776,15 +779,15 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             const int64_t at = (int64_t)max(x.pg, 0) * p.Hkv + h0;
             const float *a = p.scale[0] + at, *c = p.scale[1] + at;
             if (HG == 4 && p.vec_scales) {
-                const float4 k = __ldg(reinterpret_cast<const float4*>(a));
-                const float4 v = __ldg(reinterpret_cast<const float4*>(c));
+                const float4 k = *reinterpret_cast<const float4*>(a);
+                const float4 v = *reinterpret_cast<const float4*>(c);
                 x.ks[0] = k.x; x.ks[1 % HG] = k.y; x.ks[2 % HG] = k.z; x.ks[3 % HG] = k.w;
                 x.vs[0] = v.x; x.vs[1 % HG] = v.y; x.vs[2 % HG] = v.z; x.vs[3 % HG] = v.w;
             } else {
 #pragma unroll
                 for (int h = 0; h < HG; ++h) {
-                    x.ks[h] = __ldg(a + h);
-                    x.vs[h] = __ldg(c + h);
+                    x.ks[h] = a[h];
+                    x.vs[h] = c[h];
                 }
             }
         };
