@@ -384,6 +384,14 @@ struct AttnCfg {
     static constexpr int SMEM = BAR_AT + STAGES * 20;
 };
 
+// What a producer warp waits for before it leaves, whose units are every PRODUCERS-th up to
+// `issued` (-1: none): those whose stage it has not taken again, so whose copies may be in
+// flight.  It depends on what was issued alone, not on how many units were still to come.
+template <int STAGES, int PRODUCERS, typename Wait>
+__host__ __device__ __forceinline__ void drain(int issued, Wait&& wait) {
+    for (int j = issued; j >= 0 && j + STAGES > issued; j -= PRODUCERS) wait(j);
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -722,7 +730,6 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         int i = pw;                    // this warp's units: pw, pw + PRODUCERS, ...
         int64_t u = w.a + pw;          // the unit to look at next, inside row w.t
         int issued = -1;
-        int64_t total = w.b - w.a;     // units of the rows so far
         bool ok = true;
         int64_t tb = -1, n = 0;        // row of the cached lookup, its sequence and keys
         int b = 0;
@@ -732,7 +739,6 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             while (!w.done() && u >= w.b) {
                 u -= w.b;
                 w.next<DENSE>(p, scan);
-                total += w.b;
             }
             return !w.done();
         };
@@ -871,10 +877,11 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             next = after;
             after = last;
         }
-        // copies in flight end before the CTA does (earlier units' stages were taken again)
+        // copies in flight end before the CTA does, also where a wait gave up above
         if (lane == 0)
-            for (int j = issued; j >= 0 && j + C::STAGES >= total; j -= C::PRODUCERS)
-                if (!mbar_wait_to(p.err, smem_u32(&full[j % C::STAGES]), (j / C::STAGES) & 1)) break;
+            drain<C::STAGES, C::PRODUCERS>(issued, [&](int j) {
+                mbar_wait_to(p.err, smem_u32(&full[j % C::STAGES]), (j / C::STAGES) & 1);
+            });
         return;
     }
 
