@@ -683,7 +683,8 @@ DSA_API size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int 
  *        as DSA_DEVERR_INDEX
  *   O    [T][Hq][d] bf16 OUT (a row without keys is zeros), apart from Q
  *   lse  [T][Hq] fp32 OUT or NULL: natural log of the softmax normaliser,
- *        -inf for a row without keys
+ *        -inf for a row without keys.  A head of Q that holds an infinity or a
+ *        NaN gives NaN in both (but a row without keys its zeros and -inf)
  *   workspace: dsa_attn_kv8_workspace_size(T, k, Hq, Hkv, d) bytes; calls that
  *        may overlap on the GPU (two captured graphs included) need one each
  * Supported: d in {64, 128}, Hq / Hkv <= 8, Hkv <= 64, k <= 65536.  Scores

@@ -941,7 +941,11 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                                                         __uint_as_float(raw[i][j] & 0xffff0000u) * up);
                     qf[i][j >> 1][j & 1] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-            const float back = p.scale_log2 * __uint_as_float((uint32_t)(127 - qe) << 23);
+            // an infinity makes every score infinite or NaN, so the softmax NaN: said here, as
+            // scores that are all -inf would pass for a row without keys
+            const float back = top >= 0x7f80u
+                                   ? NAN
+                                   : p.scale_log2 * __uint_as_float((uint32_t)(127 - qe) << 23);
             qs[0] = __shfl_sync(0xffffffffu, back, 8 * t4);
             qs[1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4);
         }
