@@ -23,9 +23,11 @@ DEVERR_NONE, DEVERR_TIMEOUT, DEVERR_INDEX = 0, 1, 2
 _lib = None
 
 # the current device and its current stream's handle without the wrapper
-# objects of torch.cuda (0.2 against 3.5 us a call)
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# objects of torch.cuda (0.2 against 3.5 us a call), or through them where this
+# torch lacks these private functions (one built without CUDA does)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 class DSAError(RuntimeError):
