@@ -590,6 +590,11 @@ def _load_native():
         except ImportError as e:
             raise RuntimeError("the package's _native.so is missing or does not load; build it "
                                "with `python -m sparse_long_context_02_b200.build`") from e
+        from .build import binding_key
+        if getattr(m, "built_for", None) != binding_key():
+            raise RuntimeError(f"_native.so was built for {getattr(m, 'built_for', 'another torch')}"
+                               f", this is {binding_key()}; build it with "
+                               "`python -m sparse_long_context_02_b200.build`")
         m.bind(LIB_PATH, _check)
         _native_module = m
     return _native_module

@@ -17,6 +17,7 @@ PROBE_PATH = os.path.join(HERE, "libdsa_probe.so")
 # the Python side's argument marshalling (host code, torch's C++ API)
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(HERE, "_native.so")
+BINDING_STAMP = os.path.join(HERE, "_native.built_for")  # binding_key() of that file
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
     os.path.join(ROOT, "include", "dsa.h")]
 
@@ -44,9 +45,27 @@ def build_probe(force: bool = False) -> str:
     return PROBE_PATH
 
 
+def binding_key() -> str:
+    """What the binding depends on beside its source: it reads tensors through
+    torch's inline accessors and calls CPython's API, so it serves this torch and
+    this Python only."""
+    import torch
+    return (f"torch {torch.__version__}, C++ ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('SOABI')}")
+
+
+def _stamp() -> str:
+    try:
+        with open(BINDING_STAMP) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
 def build_binding(force: bool = False) -> str:
     deps = (BINDING_SOURCE, os.path.join(ROOT, "include", "dsa.h"))
-    if (not force and os.path.exists(BINDING_PATH)
+    key = binding_key()
+    if (not force and os.path.exists(BINDING_PATH) and _stamp() == key
             and os.path.getmtime(BINDING_PATH) >= max(os.path.getmtime(d) for d in deps)):
         return BINDING_PATH
     import torch
@@ -57,13 +76,18 @@ def build_binding(force: bool = False) -> str:
     subprocess.check_call([
         os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
         "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        f'-DDSA_BUILT_FOR="{key}"',
         "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(at, "include"),
         "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
         "-isystem", os.path.join(cuda, "include"),
         "-isystem", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SOURCE,
         "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
         "-ldl"])
+    if os.path.exists(BINDING_STAMP):  # never beside a file that it does not describe
+        os.remove(BINDING_STAMP)
     os.replace(tmp, BINDING_PATH)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(key)
     return BINDING_PATH
 
 

@@ -460,4 +460,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__native() {
+    PyObject* m = PyModule_Create(&module);
+    // the torch and the Python that it was compiled against; the package checks it
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", DSA_BUILT_FOR) != 0)
+        Py_CLEAR(m);
+    return m;
+}
