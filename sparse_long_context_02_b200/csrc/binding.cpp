@@ -97,6 +97,21 @@ Heads heads(const at::Tensor& t, const char* name, int dev, int64_t L, int64_t d
     return {t.data_ptr(), L > 1 ? t.stride(0) : H * d, H};
 }
 
+// Other Python threads run meanwhile: a launch waits where the GPU's queue is full, an
+// allocation where the memory has to come from the driver.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+template <typename... P, typename... A>
+int call(dsa_status_t (*f)(P...), A... args) {
+    const Unlocked unlocked;
+    return f(args...);
+}
+
 // The launch stream: None is the current one, else a torch.cuda.Stream or a handle.
 struct Launch {
     int dev;
@@ -125,6 +140,7 @@ struct Launch {
     }
 
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
+        const Unlocked unlocked;
         c10::cuda::OptionalCUDAStreamGuard guard;
         if (other) guard.reset_stream(*other);
         return at::empty(shape, at::TensorOptions()
@@ -235,22 +251,19 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 throw Refused(name + ": k_out has " + std::to_string(ko.heads) + " heads, k " +
                               std::to_string(hk.heads));
         }
-        const float rs = static_cast<float>(number(a[5]));
+        const float rs = static_cast<float>(number(a[5])), os = static_cast<float>(number(a[6]));
         const int off = integer(a[7]), inter = PyObject_IsTrue(a[8]) == 1;
         const int rot = 2 * static_cast<int>(freqs.numel());
-        int st;
-        if (backward)
-            st = f_rope_backward(hq.p, hk.p, static_cast<const int64_t*>(pp),
-                                 static_cast<const uint64_t*>(fp), L, (int)Hq, (int)hk.heads,
-                                 (int)d, off, rot, inter, rs, type_code(in), type_code(out),
-                                 hq.stride, hk.stride, qo.stride, ko.stride, qo.p, ko.p, err,
-                                 at_.handle);
-        else
-            st = f_rope(hq.p, hk.p, static_cast<const int64_t*>(pp),
-                        static_cast<const uint64_t*>(fp), L, (int)Hq, (int)hk.heads, (int)d, off,
-                        rot, inter, rs, static_cast<float>(number(a[6])), type_code(in),
-                        type_code(out), hq.stride, hk.stride, qo.stride, ko.stride, qo.p, ko.p,
-                        err, at_.handle);
+        const auto* positions = static_cast<const int64_t*>(pp);
+        const auto* table = static_cast<const uint64_t*>(fp);
+        const int st =
+            backward
+                ? call(f_rope_backward, hq.p, hk.p, positions, table, L, (int)Hq, (int)hk.heads,
+                       (int)d, off, rot, inter, rs, type_code(in), type_code(out), hq.stride,
+                       hk.stride, qo.stride, ko.stride, qo.p, ko.p, err, at_.handle)
+                : call(f_rope, hq.p, hk.p, positions, table, L, (int)Hq, (int)hk.heads, (int)d, off,
+                       rot, inter, rs, os, type_code(in), type_code(out), hq.stride, hk.stride,
+                       qo.stride, ko.stride, qo.p, ko.p, err, at_.handle);
         if (!done(st, name.c_str())) return nullptr;
         PyObject* r = PyTuple_New(2);
         if (r == nullptr) return nullptr;
@@ -339,12 +352,11 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Heads v = heads(V, "V", at_.dev, T, c.d, at::kBFloat16);
         if (k.heads != c.Hkv || v.heads != c.Hkv)
             throw Refused("K and V must have " + std::to_string(c.Hkv) + " heads");
-        const int st = f_append(k.p, v.p, T, k.stride, v.stride, c.k8, c.v8, c.ks, c.vs, c.pages,
-                                (int)c.page, c.table, (int)c.M, c.lens,
-                                offsets(a[8], "new_off", c.B, at_.dev), (int)c.B, (int)c.Hkv,
-                                (int)c.d,
-                                dense_or_null<int32_t>(a[10], "err", at_.dev, at::kInt, 1),
-                                at_.handle);
+        const int32_t* new_off = offsets(a[8], "new_off", c.B, at_.dev);
+        int32_t* err = dense_or_null<int32_t>(a[10], "err", at_.dev, at::kInt, 1);
+        const int st = call(f_append, k.p, v.p, T, k.stride, v.stride, c.k8, c.v8, c.ks, c.vs,
+                            c.pages, (int)c.page, c.table, (int)c.M, c.lens, new_off, (int)c.B,
+                            (int)c.Hkv, (int)c.d, err, at_.handle);
         if (!done(st, "dsa_kv8_append")) return nullptr;
         Py_RETURN_NONE;
     });
@@ -407,12 +419,12 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const size_t wb = ws.defined() ? ws.nbytes() : 0;
         const float scale = static_cast<float>(number(a[8]));
         const int st =
-            sparse ? f_sparse(q, c.k8, c.v8, c.ks, c.vs, c.pages, (int)c.page, c.table, (int)c.M,
-                              c.lens, row_off, (int)c.B, T, idx, (int)keys, (int)Hq, (int)c.Hkv,
-                              (int)c.d, scale, o, lse, wp, wb, err, at_.handle)
-                   : f_dense(q, c.k8, c.v8, c.ks, c.vs, c.pages, (int)c.page, c.table, (int)c.M,
-                             c.lens, row_off, (int)c.B, T, (int)Hq, (int)c.Hkv, (int)c.d, scale, o,
-                             lse, wp, wb, err, at_.handle);
+            sparse ? call(f_sparse, q, c.k8, c.v8, c.ks, c.vs, c.pages, (int)c.page, c.table,
+                          (int)c.M, c.lens, row_off, (int)c.B, T, idx, (int)keys, (int)Hq,
+                          (int)c.Hkv, (int)c.d, scale, o, lse, wp, wb, err, at_.handle)
+                   : call(f_dense, q, c.k8, c.v8, c.ks, c.vs, c.pages, (int)c.page, c.table,
+                          (int)c.M, c.lens, row_off, (int)c.B, T, (int)Hq, (int)c.Hkv, (int)c.d,
+                          scale, o, lse, wp, wb, err, at_.handle);
         if (!done(st, sparse ? "dsa_sparse_attn_kv8" : "dsa_attn_kv8")) return nullptr;
         return a[10] != Py_None ? Py_NewRef(a[10]) : THPVariable_Wrap(O);
     });
