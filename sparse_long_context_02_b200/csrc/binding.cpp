@@ -252,7 +252,8 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                               std::to_string(hk.heads));
         }
         const float rs = static_cast<float>(number(a[5])), os = static_cast<float>(number(a[6]));
-        const int off = integer(a[7]), inter = PyObject_IsTrue(a[8]) == 1;
+        const int off = integer(a[7]), inter = PyObject_IsTrue(a[8]);
+        if (inter < 0) throw std::runtime_error("interleaved has no truth value");
         const int rot = 2 * static_cast<int>(freqs.numel());
         const auto* positions = static_cast<const int64_t*>(pp);
         const auto* table = static_cast<const uint64_t*>(fp);

@@ -79,3 +79,19 @@ def test_other_threads_run_during_a_call(tmp_path):
     assert r.returncode == 0, r.stderr[-2000:]
     lines = r.stdout.split("\n")
     assert sum("ran beside another thread" in line for line in lines) == 5, r.stdout
+
+
+def _rope_args(L=2, H=4, d=64):
+    return (torch.zeros((L, H, d), dtype=torch.bfloat16, device="cuda"), None,
+            torch.zeros(L, dtype=torch.int64, device="cuda"), dsa.rope_freqs(d)[0])
+
+
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    for call in (dsa.rope, dsa.rope_backward):
+        with pytest.raises(KeyError, match="neither"):
+            call(*_rope_args(), interleaved=Neither())
+    dsa.rope(*_rope_args(), interleaved=True)
