@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -158,7 +159,8 @@ bool done(int status, const char* name) {
     return false;
 }
 
-// Runs a call's body; C++ exceptions end here.
+// Runs a call's body; C++ exceptions end here, torch's as the Python exceptions that it
+// has for them (an allocation that does not fit as torch.OutOfMemoryError).
 template <typename F>
 PyObject* guarded(F&& body) {
     try {
@@ -166,8 +168,8 @@ PyObject* guarded(F&& body) {
     } catch (const Refused& e) {
         PyErr_Clear();
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception& e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -95,3 +95,21 @@ def test_a_flag_without_a_truth_value_raises_its_own_error():
         with pytest.raises(KeyError, match="neither"):
             call(*_rope_args(), interleaved=Neither())
     dsa.rope(*_rope_args(), interleaved=True)
+
+
+def test_out_of_memory_is_torchs_error():
+    """An output that does not fit raises what torch.empty raises, which callers
+    catch to retry with less."""
+    q = torch.empty((1 << 20, 4, 64), dtype=torch.bfloat16, device="cuda")  # 512 MB
+    pos = torch.zeros(1 << 20, dtype=torch.int64, device="cuda")
+    f = dsa.rope_freqs(64)[0]
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction(
+        (torch.cuda.memory_reserved() + (64 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            dsa.rope(q, None, pos, f)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert dsa.rope(q[:8], None, pos[:8], f)[0].shape == (8, 4, 64)
