@@ -636,8 +636,9 @@ DSA_API dsa_status_t dsa_rope_backward(const void* dq, const void* dk, const int
  *   K, V  [T][Hkv][d] bf16; row r starts at element r * k_stride (r * v_stride),
  *         strides multiples of 8
  *   new_off [B + 1] int32 device: rows [new_off[b], new_off[b + 1]) are
- *         sequence b's, ascending from 0 to at most T; or NULL: T = B, one
- *         row for each sequence.  Rows past new_off[B] are ignored.
+ *         sequence b's, ascending from 0 to at most T (else recorded as
+ *         DSA_DEVERR_INDEX, and what is stored is not defined); or NULL: T = B,
+ *         one row for each sequence.  Rows past new_off[B] are ignored.
  *   seq_lens[b] < 0: an idle place of the batch, skipped with its rows.
  * Per page, head and tensor: need = the smallest power of two (2^-120 at
  * least) with max |new finite elements on the page| <= 448 need; the scale
@@ -674,7 +675,8 @@ DSA_API size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int 
  *   Q    [T][Hq][d] bf16
  *   row_off [B + 1] int32 device: rows [row_off[b], row_off[b + 1]) are
  *        sequence b's (a chunk of its prompt, or several tokens decoded at
- *        once), row_off[0] = 0, ascending, at most T; or NULL: T = B, one row
+ *        once), row_off[0] = 0, ascending, at most T (else recorded as
+ *        DSA_DEVERR_INDEX, and the rows are not defined); or NULL: T = B, one row
  *        for each sequence.  O and lse of rows past row_off[B] are not written.
  *   seq_lens [B]: stored tokens, the rows' own included; <= 0: no keys
  *   idx  [T][k] int32: positions in the row's sequence (such as

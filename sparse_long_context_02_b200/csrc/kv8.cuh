@@ -39,6 +39,14 @@ struct Rows {
     int64_t n;           // rows of the arrays
 };
 
+// Records offsets of sequence b that do not ascend or lead past the arrays.  The lookups
+// check the pair that they find, but where offsets run backwards a search need not come to
+// every pair, so a launch looks at all of them.
+__device__ __forceinline__ void check_offsets(const Rows& rw, int* err, int b) {
+    const int32_t first = rw.off[b], end = rw.off[b + 1];
+    if (first < 0 || end < first || end > rw.n) record_error_to(err, 2);
+}
+
 // ------------------------------------------------------------------ append
 
 struct AppendParams {
@@ -182,6 +190,11 @@ append_kernel(const AppendParams p, int units) {
     using C = AppendCfg<PAGE, D>;
     __shared__ uint32_t top_s[kAppendThreads / 32];
     pdl_wait();
+    // a thread for every sequence: the grid covers 2 B units, 2 tensors and the heads
+    if (blockIdx.x <= p.rows.B / kAppendThreads) {
+        const int b = blockIdx.x * kAppendThreads + threadIdx.x;
+        if (b < p.rows.B) check_offsets(p.rows, p.err, b);
+    }
     const int warp = threadIdx.x >> 5, team = warp / C::TEAM;
     const int me = threadIdx.x - team * C::TEAM * 32;  // thread of the team
     const uint32_t item = blockIdx.x * C::TEAMS + team, hkv = p.Hkv;  // below 2^31 + 8
@@ -877,6 +890,11 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
             next = after;
             after = last;
         }
+        if (pw == 0 && blockIdx.y == 0 && p.rows.off != nullptr)
+            // here, as the consumers have no registers to spare and are not done yet
+#pragma unroll 1
+            for (int seq = blockIdx.x * 32 + lane; seq < p.rows.B; seq += gridDim.x * 32)
+                check_offsets(p.rows, p.err, seq);
         // copies in flight end before the CTA does, also where a wait gave up above
         if (lane == 0)
             drain<C::STAGES, C::PRODUCERS>(issued, [&](int j) {
