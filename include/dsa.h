@@ -660,8 +660,12 @@ DSA_API dsa_status_t dsa_kv8_append(const void* K, const void* V, int64_t T, int
  * dsa_attn_kv8_workspace_size - bytes of device workspace (16-byte aligned;
  * not read before it is written) for T query rows over at most `keys` keys
  * each: k for dsa_sparse_attn_kv8, max_pages * page for dsa_attn_kv8.  May be
- * 0 (the workspace may then be NULL).
+ * 0 (the workspace may then be NULL).  dsa_attn_kv8 with T >
+ * DSA_ATTN_KV8_CUT_ROWS needs none whatever this returns: it deals its rows out
+ * whole, in their order, instead of cutting all keys into equal parts, so one
+ * row far longer than the others is then a single SM's work.
  */
+#define DSA_ATTN_KV8_CUT_ROWS 512
 DSA_API size_t dsa_attn_kv8_workspace_size(int64_t T, int64_t keys, int Hq, int Hkv, int d);
 
 /*

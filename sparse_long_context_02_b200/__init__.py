@@ -661,7 +661,8 @@ def kv8_append(K: torch.Tensor, V: torch.Tensor, k8: torch.Tensor, v8: torch.Ten
 
 def attn_kv8_workspace_size(T: int, keys: int, Hq: int, Hkv: int, d: int) -> int:
     """Bytes of workspace for T rows over at most `keys` keys each: k for
-    sparse_attn_kv8, block_table columns x page for attn_kv8."""
+    sparse_attn_kv8, block_table columns x page for attn_kv8 (which needs none
+    for more than 512 rows)."""
     return lib().dsa_attn_kv8_workspace_size(T, keys, Hq, Hkv, d)
 
 

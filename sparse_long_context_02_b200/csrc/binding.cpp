@@ -414,7 +414,7 @@ PyObject* py_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
         at::Tensor ws;
         if (a[12] != Py_None) {
             ws = tensor(a[12], "workspace");
-        } else {
+        } else if (sparse || T <= DSA_ATTN_KV8_CUT_ROWS) {
             const size_t need = f_workspace(T, keys, (int)Hq, (int)c.Hkv, (int)c.d);
             if (need > 0) ws = at_.empty({(int64_t)need}, at::kByte);
         }

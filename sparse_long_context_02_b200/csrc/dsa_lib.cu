@@ -1773,7 +1773,10 @@ dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const v
     if (lse != nullptr) CHECK_PTR4(lse);
     const int64_t cap = sparse ? k : (int64_t)max_pages * page;
     const Kv8Plan pl = kv8_plan(T, cap, Hq, Hkv, d);
-    if (pl.total > 0) {
+    static_assert(dsa::kv8::kMaxScan == DSA_ATTN_KV8_CUT_ROWS, "");
+    const bool whole_rows = pl.cluster == 0 && !sparse && T > dsa::kv8::kMaxScan;
+    const bool merge = pl.total > 0 && !whole_rows;  // the only use of the workspace
+    if (merge) {
         CHECK_PTR(workspace);
         if (workspace_bytes < pl.total)
             return fail(DSA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes,
@@ -1798,10 +1801,9 @@ dsa_status_t run_attn_kv8(const char* fn, const void* Q, const void* K8, const v
     p.scale_log2 = scale * 1.4426950408889634f;
     p.vec_scales = aligned16(k_scale) && aligned16(v_scale);
     p.cluster = pl.cluster;
-    p.whole_rows = pl.cluster == 0 && !sparse && T > dsa::kv8::kMaxScan;
+    p.whole_rows = whole_rows;
     p.O = static_cast<__nv_bfloat16*>(O);
     p.lse = lse;
-    const bool merge = pl.total > 0 && !p.whole_rows;
     if (merge) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.part_o = reinterpret_cast<float*>(ws);
