@@ -388,6 +388,7 @@ struct AttnCfg {
     // parity only tells neighbouring phases apart, so whoever waits for a phase has to have
     // waited for (or caused) the one before it.
     static_assert(STAGES % PRODUCERS == 0 && STAGES % NSUB == 0, "");
+    static_assert(NSUB > 1, "the warps of a head join their sums behind a barrier");
     static constexpr int OROW = D + 4;
     static constexpr int O_AT = STAGES * STAGE;
     static constexpr int SC_AT = O_AT + (kConsumers - HG) * 8 * OROW * 4;
@@ -976,7 +977,7 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
         float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
         for (int64_t u = w.a; u < w.b; ++u, ++done) {
-            if (C::NSUB > 1 && done % C::NSUB != sub) continue;
+            if (done % C::NSUB != sub) continue;
             const int st = done % C::STAGES;
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_to(p.err, smem_u32(&full[st]),
                                                               (done / C::STAGES) & 1));
@@ -1101,22 +1102,22 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
         constexpr int DT = 2 * MT;  // d of a thread: DT g .. DT g + DT - 1, o[i][c] and o[i][c + 2]
-        if (C::NSUB > 1) {
-            named_bar_sync(1, kConsumers * 32);  // the row before has been read
-            if (sub > 0) {
+        named_bar_sync(1, kConsumers * 32);  // the row before has been read
+        if (sub > 0) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float* q = o_s + ((warp - HG) * 8 + 2 * t4 + c) * C::OROW + DT * g;
+            for (int c = 0; c < 2; ++c) {
+                float* q = o_s + ((warp - HG) * 8 + 2 * t4 + c) * C::OROW + DT * g;
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        q[2 * i] = o[i][c];
-                        q[2 * i + 1] = o[i][c + 2];
-                    }
-                    if (g == 0) m_s[warp * 8 + 2 * t4 + c] = make_float4(mx[c], my[c], l[c], 0.f);
+                for (int i = 0; i < MT; ++i) {
+                    q[2 * i] = o[i][c];
+                    q[2 * i + 1] = o[i][c + 2];
                 }
+                if (g == 0) m_s[warp * 8 + 2 * t4 + c] = make_float4(mx[c], my[c], l[c], 0.f);
             }
-            named_bar_sync(1, kConsumers * 32);
         }
+        // the others' sums are there; nobody reads the ring for this row any more, where a
+        // cluster's go below
+        named_bar_sync(1, kConsumers * 32);
         const bool whole = w.a == 0 && w.b == w.all;
         if (p.part_row != nullptr && threadIdx.x == 0 && blockIdx.y == 0 && w.a == 0) {
             // for the merge: the CTAs of this row, named by the one that has its first unit
@@ -1129,10 +1130,6 @@ attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                 p.part_row[w.t] = make_int4(r.x, r.x < 0 ? 0 : (int)blockIdx.x, r.y, 0);
             else
                 last = r;
-        }
-        if (p.cluster > 1) {
-            // the other heads' warps may still read the ring, where the sums go next
-            named_bar_sync(2, kConsumers * 32);
         }
         if (sub > 0) continue;
         bool write = true;
