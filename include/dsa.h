@@ -543,8 +543,8 @@ DSA_API dsa_status_t dsa_indexer_kl_backward(const void* q_I, const void* k_I, c
  *     y_a = rot_scale (x_a cos th - x_b sin th)
  *     y_b = rot_scale (x_b cos th + x_a sin th)
  * the other elements pass through, and everything is multiplied by out_scale.
- * fp32 throughout, one rounding at the end; the angle is reduced exactly at
- * every 64-bit position.
+ * fp32 throughout, one rounding at the end; the angle, the product of position
+ * and table entry (below), is reduced exactly at every 64-bit position.
  *
  * Element types of the calls below.
  */
@@ -558,8 +558,11 @@ DSA_API dsa_status_t dsa_indexer_kl_backward(const void* q_I, const void* k_I, c
 #define DSA_ROPE_NTK 2           /* base * factor^(rot / (rot - 2)) as the base */
 #define DSA_ROPE_YARN 3          /* Peng et al., arXiv 2309.00071: w_i / factor where a pair turns
                                     fewer than beta_slow times over orig_len positions, w_i where
-                                    more than beta_fast times, linear in between; rot_scale =
-                                    0.1 ln(factor) + 1 */
+                                    more than beta_fast times, linear in the number of turns in
+                                    between, as the paper has it; rot_scale = 0.1 ln(factor) + 1.
+                                    Other programs make the ramp linear in the pair's index i
+                                    between two rounded bounds: a model trained with that needs a
+                                    table filled by the caller */
 
 /*
  * dsa_rope_freqs - the frequency table of the rotary calls (host function, no
@@ -589,7 +592,7 @@ DSA_API dsa_status_t dsa_rope_freqs(int rot, double base, int scaling, double fa
  * d, offset, rot even, offset + rot <= d <= 1024, Hq + Hk <= 1024.  Pointers
  * aligned to their elements suffice; 16-byte alignment of pointers and
  * strides and d, offset and rot multiples of 16 (F32: 8) run fastest.  L = 0 does
- * nothing.
+ * nothing.  The kernels have nothing to record in err.
  */
 DSA_API dsa_status_t dsa_rope(const void* q, const void* k, const int64_t* positions,
                               const uint64_t* freqs, int64_t L, int Hq, int Hk, int d,
@@ -714,7 +717,9 @@ DSA_API dsa_status_t dsa_sparse_attn_kv8(const void* Q, const void* K8, const vo
  * (causal).  For layers or stages that keep the full attention, and contexts
  * no longer than the selection.  Made for single tokens and a few tokens at
  * once: every row reads its keys anew.  Arguments and support as
- * dsa_sparse_attn_kv8, without idx; workspace for max_pages * page keys.
+ * dsa_sparse_attn_kv8, without idx; workspace for max_pages * page keys.  How the
+ * work is divided follows that width of the table, not the lengths: short
+ * sequences run fastest in a table no wider than they need.
  */
 DSA_API dsa_status_t dsa_attn_kv8(const void* Q, const void* K8, const void* V8,
                                   const float* k_scale, const float* v_scale, int64_t num_pages,

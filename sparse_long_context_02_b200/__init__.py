@@ -605,7 +605,9 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
                device=None):
     """The frequency table of the rotary calls (rot / 2 int64 on the device:
     turns per position in units of 2^-64) and the factor on the rotated part
-    (`rot_scale`).  scaling: "none", "linear", "ntk" or "yarn"."""
+    (`rot_scale`).  scaling: "none", "linear", "ntk" or "yarn", whose ramp is
+    linear in a pair's turns as in the paper (a model trained with a ramp over
+    the pair's index needs a table of its own)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"rope_freqs: scaling must be one of {sorted(ROPE_SCALINGS)}")
     freqs = torch.empty(max(0, int(rot)) // 2, dtype=torch.int64)
@@ -689,7 +691,8 @@ def attn_kv8(Q: torch.Tensor, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch
              O: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None, stream=None, err=None) -> torch.Tensor:
     """sparse_attn_kv8 over every key of the sequence; with row_off, where the
-    rows are a sequence's last tokens, causally."""
+    rows are a sequence's last tokens, causally.  The work is divided by the
+    width of the block table, and more than 512 rows are dealt out whole."""
     return (_native_module or _load_native()).attn_kv8(Q, k8, v8, k_scale, v_scale, block_table,
                                                   seq_lens, None, scale, row_off, O, lse,
                                                   workspace, stream, err)

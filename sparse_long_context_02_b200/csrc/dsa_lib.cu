@@ -1627,8 +1627,11 @@ Kv8Plan kv8_plan(int64_t T, int64_t cap, int Hq, int Hkv, int d) {
     const int sms = num_sms();
     const int64_t per = (cap + dsa::kv8::kKeys - 1) / dsa::kv8::kKeys;  // units of a row
     // Few rows of up to 32 units per CTA: a row per cluster, joined through shared memory,
-    // which saves the second kernel and its launch (one row of 2048 keys 8.1 us against 9.3,
-    // 64 such rows 31.3 against 38, 100 of 1024 26.6 against 32).  Not longer ones: rows of
+    // which saves the second kernel and its launch (device time of 1, 16, 38, 50 and 64 rows of
+    // 2048 keys 7.7, 12.6, 28.9, 30.1 and 32.6 us against 9.3, 15.7, 28.0, 32.3 and 39.0 in
+    // equal ranges; 64, 75, 100 and 148 of 1024 20.8, 26.9, 27.9 and 34.4 against 27.5, 27.2,
+    // 31.6 and 36.0; 37 and 148 of 512 9.0 and 20.9 against 12.6 and 22.4: also where SMs stay
+    // idle, but for 3 % at 38 rows).  Not longer ones: rows of
     // very different lengths are what the equal ranges below are for.  As many CTAs per row
     // as run at once: a second wave of clusters doubles the time (16 rows of 2048 keys in
     // clusters of 8: 26.9 us where 15 fit, 12.6 in clusters of 4).  One KV head per CTA

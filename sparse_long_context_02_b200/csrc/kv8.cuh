@@ -182,8 +182,9 @@ struct AppendCfg {
 // heads side by side.  The page's new elements stay in registers between the
 // maximum and the rounding, so they are read once; their loads go out before the
 // page is looked up, eight (four) of 16 bytes per thread.  A chunk of 32768 rows of
-// 4 x 128 takes 20.3 us (5.0 TB/s), with teams twice as large 20.9; issue slots are
-// 72 % busy.
+// 4 x 128 takes 20.1 us (5.0 TB/s), with teams twice as large 20.9; issue slots are
+// 60 % and the ALU pipe 56 % busy (maxima, conversions) in three and a half waves of
+// four CTAs per SM.
 template <int PAGE, int D>
 __global__ void __launch_bounds__(kAppendThreads, AppendCfg<PAGE, D>::VPT == 4 ? 6 : 4)
 append_kernel(const AppendParams p, int units) {
@@ -643,24 +644,26 @@ __device__ __forceinline__ void merge_cluster(const AttnParams& p, const uint8_t
 // them, one per head, at each unit, the others at the units between.
 //
 // Measured on 32/4 heads of 128 (device time).  Over every key, 8 rows of 16K to
-// 128K keys: 94.6 us, 6.07 TB/s of codes (93 % of a copy's rate), bound by HBM.  64 rows
-// of 2048 selected keys: 31.3 us, 4.3 TB/s, bound by HBM's rate for 512-byte pieces (5 TB/s
-// with more rows) and a start of dependent loads (index row, table, codes).  1000 rows of
-// one chunk over a cache that fits L2: 285 us, 7.4 TB/s of gathered codes; issue slots
-// are 53 % and the ALU pipe 49 % busy (widening codes takes half of it) with 11 warps per
-// SM, all that 168 registers allow; the copies alone take 234 us with four producers.
-// One row of 2048: 7.9 us, latency.  Loads straight to registers, 16 warps per SM
-// without a ring, took 242.6, 63.9, 444.9 and 11.5.
+// 128K keys: 95.8 us, 6.0 TB/s of codes (92 % of a copy's rate), bound by HBM.  64 rows
+// of 2048 selected keys: 31.0 us, 4.4 TB/s: the keys at HBM's rate for 512-byte pieces
+// (24 us at the 5.6 TB/s that 300 rows and 600 rows reach) behind a single row's chain of
+// dependent loads (index row, table, codes).  1000 rows of one chunk over a cache that fits
+// L2: 285 us, 7.4 TB/s of gathered codes; issue slots are 54 % and the ALU pipe 49 % busy
+// (widening codes takes half of it) with 11 warps per SM (a twelfth would fit 168
+// registers, but six stages of 32 KB do not divide among four producers); the copies alone
+// take 234 us with four producers.  One row of 2048: 7.8 us, latency.  Loads straight to
+// registers, 16 warps per SM without a ring, took 242.6, 63.9, 444.9 and 11.5.
 // Tried and slower: e4m3 operands on mma.sync, which converts inside (24 cycles against
 // 8.4 for fp16's with fresh operands); V read transposed by ldmatrix b8 instead of byte
 // permutes (305 us on the chunk against 295, for want of registers); 16 consumer warps
 // (408, spills); the next unit's scores beside this one's softmax (354, holds stages).
 //
 // Copies.  Selected keys are gathered with 16-byte cp.async, a warp taking a
-// key's HG * d bytes at once (one bulk copy for each
-// row this short keeps the copy engine from the rate that the load path reaches); over every key a unit lies inside a page and comes as one TMA box
-// per head.  Either way a head's 32 rows of d bytes lie with their 16-byte
-// pieces exclusive-or'ed by the row, as TMA's swizzle does.
+// key's HG * d bytes at once (one bulk copy for each row this short keeps the copy
+// engine from the rate that the load path reaches).  Over every key a unit comes as
+// one TMA box per head, or as two where it covers two pages of 16.  Either way a
+// head's 32 rows of d bytes lie with their 16-byte pieces exclusive-or'ed by the
+// row, as TMA's swizzle does.
 //
 // S^T = K Q^T: 16 keys are the rows of an m16n8k16 product, the head group's
 // queries (up to 8) its columns.  The sum over d may run in any order, so thread
