@@ -3,6 +3,8 @@ import os
 import subprocess
 import sys
 
+from sparse_long_context_02_b200 import build as dsa_build
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -15,6 +17,7 @@ def _run(code):
 def test_import_where_torch_has_no_cuda_bindings():
     """A torch built without CUDA has no torch._C._cuda_*: the import, the host
     functions and the refusals of host tensors work there."""
+    dsa_build.build()
     out = _run("""
 import torch
 for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
