@@ -113,3 +113,56 @@ def test_out_of_memory_is_torchs_error():
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert dsa.rope(q[:8], None, pos[:8], f)[0].shape == (8, 4, 64)
+
+
+def test_threads_with_streams_of_their_own():
+    """Four threads call at once, each on its stream and its cache: every result
+    is the one that the same calls give alone."""
+    import threading
+
+    def work(seed, stream):
+        with torch.cuda.stream(stream):
+            g = torch.Generator(device="cuda").manual_seed(seed)
+            B, Hq, Hkv, d, page, M = 5 + 60 * (seed % 2), 8, 2, 64, 16, 700
+            pools = [torch.zeros((B * 8, page, Hkv, d), dtype=torch.uint8, device="cuda")
+                     for _ in "kv"]
+            scales = [torch.zeros((B * 8, Hkv), device="cuda") for _ in "kv"]
+            table = torch.full((B, M), -1, dtype=torch.int32, device="cuda")
+            table[:, :8] = torch.arange(B * 8, device="cuda").reshape(B, 8)
+            lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+            freqs = dsa.rope_freqs(d)[0]
+            idx = torch.arange(16, dtype=torch.int32, device="cuda").repeat(B, 1)
+            err = dsa.error_word()
+            out = []
+            for step in range(40):
+                x = torch.randn((B, Hq + 2 * Hkv, d), generator=g, device="cuda").bfloat16()
+                q, k = dsa.rope(x[:, :Hq], x[:, Hq:Hq + Hkv], lens.long(), freqs)
+                dsa.kv8_append(k, x[:, Hq + Hkv:], *pools, *scales, table, lens, err=err)
+                lens = lens + 1
+                O = dsa.attn_kv8(q, *pools, *scales, table, lens, 0.125, err=err)
+                rows = torch.where(idx < lens[:, None], idx, -1)
+                S = dsa.sparse_attn_kv8(O, *pools, *scales, table, lens, rows, 0.125, err=err)
+                out += [O, S]
+            out += pools + scales
+            stream.synchronize()
+            assert dsa.device_error(err=err) == dsa.DEVERR_NONE
+            return out
+
+    want = [work(seed, torch.cuda.Stream()) for seed in range(4)]
+    got, failed = [None] * 4, []
+
+    def run(seed):
+        try:
+            got[seed] = work(seed, torch.cuda.Stream())
+        except BaseException as e:
+            failed.append(e)
+
+    for _ in range(3):
+        threads = [threading.Thread(target=run, args=(seed,)) for seed in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not failed
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
