@@ -6,6 +6,10 @@ This module is the Python binding of ``libdsa_b200.so`` (C ABI in
 every step of the computation runs in the library's CUDA kernels.  PyTorch
 only provides device memory and streams.  There is no fallback: if the
 library is missing, calls raise.
+
+Calls are asynchronous and run on the current stream, or on `stream`.  Tensors
+whose memory belongs to another stream than that have to stay alive until the
+call has run there (Tensor.record_stream tells the allocator).
 """
 from __future__ import annotations
 
